@@ -1,0 +1,472 @@
+"""The attention path around an 8-bit key-value cache and a tree of drafted
+tokens, as measured cases.
+
+Four operators, in the order in which a decode step uses them:
+
+  qk          norms of queries and keys for each head with the position
+              rotation in the same pass, forward and backward
+  cache       new keys and values written into a cache (in 8 bits with a scale
+              per token and head, or in bf16 as they are), and an 8-bit cache
+              read back as bf16 for a prompt chunk's attention
+  decode_kv8  attention of a few new tokens over an 8-bit cache
+  tree        attention of a tree of drafted tokens over a bf16 cache
+
+``run`` computes them in their plain form (elementary torch operations in 32
+bits, angles in 64) or, where ``own`` is set, through the package's calls.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+EPS = 1e-5
+E4M3_MAX = 448.0
+
+
+# ------------------------------------------------------------------ cases
+
+def _qk(name, T, nq, nkv, d, rot, layout="half", norm=True, far=0, back=False, t=1, past=0):
+    return {"name": name, "op": "qk", "T": T, "nq": nq, "nkv": nkv, "d": d, "rot": rot,
+            "layout": layout, "norm": norm, "far": far, "back": back, "t": t, "past": past}
+
+
+def _cache(name, what, T, past, nq, nkv, d, n=0, t=1):
+    return {"name": name, "op": "cache", "what": what, "T": T, "past": past, "nq": nq,
+            "nkv": nkv, "d": d, "n": n, "t": t}
+
+
+def _attn(name, op, T, past, nq, nkv, mask, t=1):
+    return {"name": name, "op": op, "T": T, "past": past, "nq": nq, "nkv": nkv, "d": 128,
+            "mask": mask, "t": t}
+
+
+def listed():
+    return [
+        # one decoded token after a 64K-token context: latency of the smallest call
+        _qk("qk_decode_t1", 1, 64, 8, 128, 128, t=8, past=65536),
+        # drafted tokens at far positions, an odd head size, interleaved pairs, partial rotation
+        _qk("qk_ragged_far", 333, 28, 4, 80, 32, layout="pairs", far=1 << 20),
+        # a 4096-token prompt of the 70B head layout
+        _qk("qk_prompt_4096", 4096, 64, 8, 128, 128, t=8),
+        # the same in training: gradients of the inputs and of both norm weights
+        _qk("qk_backward_4096", 4096, 64, 8, 128, 128, back=True, t=8),
+        # a 4096-token prompt's keys and values written into an 8-bit cache
+        _cache("cache_append8_4096", "append8", 4096, 1000, 64, 8, 128, t=8),
+        # 64K cached tokens read back as bf16 before a prompt chunk's attention
+        _cache("cache_read8_65536", "read8", 1, 65536, 64, 8, 128, t=8),
+        # one token over a short 8-bit cache: latency
+        _attn("decode_kv8_t1_1000", "decode_kv8", 1, 1000, 64, 8, "causal", t=8),
+        # the 70B decode workload's longest call over an 8-bit cache
+        _attn("decode_kv8_t4_65536", "decode_kv8", 4, 65536, 64, 8, "causal", t=8),
+        # a drafted tree verified over an 8-bit cache, other head ratio, odd length
+        _attn("decode_kv8_tree_t21_16385", "decode_kv8", 21, 16385, 28, 4, "tree", t=4),
+        # a small drafted tree over a short bf16 cache: latency
+        _attn("tree_t7_513", "tree", 7, 513, 64, 8, "tree", t=8),
+        # an ordinary drafted tree, cache length off every block boundary
+        _attn("tree_t26_8191", "tree", 26, 8191, 64, 8, "tree", t=8),
+        # a large drafted tree over the 64K-token cache of the 70B decode workload
+        _attn("tree_t64_65536", "tree", 64, 65536, 64, 8, "tree", t=8),
+    ]
+
+
+HEADS = [(64, 8), (32, 8), (32, 32), (16, 2), (28, 4), (40, 8), (16, 1), (9, 3)]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["qk", "cache", "decode_kv8", "tree"])
+    nq, nkv = rng.choice(HEADS)
+    t = rng.choice([k for k in (1, 2, 4, 8) if nq % k == 0 and nkv % k == 0])
+    if op == "qk":
+        d = rng.choice([16, 64, 80, 96, 128, 128, 256])
+        T = _log_int(rng, 1, 4096 if d <= 128 else 2048)
+        rot = 16 * rng.randint(0, d // 16)
+        # without a norm and without a rotation there is nothing to compute
+        norm = rng.random() < 0.7 or rot == 0
+        return {**_qk("", T, nq, nkv, d, rot, rng.choice(["half", "pairs"]), norm,
+                      rng.choice([0, 0, 1 << 12, 1 << 20]), rng.random() < 0.4, t,
+                      _log_int(rng, 1, 65536))}
+    if op == "cache":
+        what = rng.choice(["append8", "append8_rows", "append16_rows", "append16", "read8"])
+        d = rng.choice([16, 64, 80, 128, 128, 256])
+        T = _log_int(rng, 1, 4096)
+        past = _log_int(rng, 1, 65536 if d * nkv <= 1024 else 8192)
+        return _cache("", what, T, past, nq, nkv, d,
+                      rng.randint(1, T) if what.endswith("rows") else 0, t)
+    T = _log_int(rng, 1, 128)
+    most = 65536 * 4096 // (T * nq)
+    past = rng.choice([0, _log_int(rng, 1, min(65536, most)), _log_int(rng, 1, min(65536, most))])
+    return _attn("", op, T, past, nq, nkv, rng.choice(["causal", "tree"]), t)
+
+
+# ------------------------------------------------------------------ inputs
+
+def _tree_words(T, rng):
+    """Visibility words [T, ceil(T / 64)] of a random drafted tree: a token sees
+    itself and its ancestors."""
+    rows = []
+    for i in range(T):
+        parent = -1 if i == 0 else rng.choice([i - 1, rng.randint(-1, i - 1), rng.randint(i // 2, i) - 1])
+        rows.append((rows[parent] if parent >= 0 else 0) | (1 << i))
+    words = (T + 63) // 64
+    signed = lambda v: v - (1 << 64) if v >> 63 else v  # noqa: E731
+    return torch.tensor([[signed((r >> (64 * w)) & ((1 << 64) - 1)) for w in range(words)]
+                         for r in rows], dtype=torch.int64)
+
+
+def _quantised(x):
+    """8-bit codes (uint8) and fp32 scales of bf16 rows: scale = max |row| / 448,
+    1 for a row of zeros."""
+    xf = x.float()
+    amax = xf.abs().amax(-1)
+    scale = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax))
+    q = (xf / scale[..., None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+    return q.view(torch.uint8), scale
+
+
+def prepare(case, seed):
+    c = case
+    T, nq, nkv, d, past = c["T"], c["nq"], c["nkv"], c["d"], c["past"]
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(seed)
+    host = random.Random(seed)
+    randn = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
+    s = {"case": c}
+    if c["op"] == "qk":
+        # projections' outputs have no fixed scale: heads of different sizes
+        size = torch.exp(0.5 * randn(1, nq + 2 * nkv, 1))
+        s["qkv"] = (randn(T, nq + 2 * nkv, d) * size).to(torch.bfloat16).reshape(T, -1)
+        s["gamma_q"] = (1 + 0.1 * randn(d)).to(torch.bfloat16) if c["norm"] else None
+        s["gamma_k"] = (1 + 0.1 * randn(d)).to(torch.bfloat16) if c["norm"] else None
+        half = c["rot"] // 2
+        s["inv_freq"] = (500000.0 ** (-torch.arange(half, device=dev, dtype=torch.float64)
+                                      / max(half, 1))).float() if half else None
+        s["positions"] = torch.randint(0, c["far"], (T,), generator=g, device=dev,
+                                       dtype=torch.int32) if c["far"] else None
+        if c["back"]:
+            s["dout"] = randn(T, (nq + 2 * nkv) * d).to(torch.bfloat16)
+        else:
+            s["out"] = torch.empty_like(s["qkv"])
+        return s
+    qkv = randn(T, nq + 2 * nkv, d)
+    if c["op"] != "cache":
+        qkv[:, :nq] *= 2.0  # scores of standard deviation two: some weights stand out
+    s["qkv"] = qkv.to(torch.bfloat16).reshape(T, -1)
+    # append writes T (or n) rows after `past`; read takes the rows before it
+    max_len = past + T + 5
+    if c["op"] == "cache" and c["what"] == "read8":
+        max_len = past + 5
+    k = torch.zeros(nkv, max_len, d, dtype=torch.bfloat16, device=dev)
+    v = torch.zeros(nkv, max_len, d, dtype=torch.bfloat16, device=dev)
+    if past:
+        # channels of a key cache differ in size far more than a value cache's
+        k[:, :past] = (randn(nkv, past, d) * torch.exp(0.3 * randn(nkv, 1, d))).to(torch.bfloat16)
+        v[:, :past] = randn(nkv, past, d).to(torch.bfloat16)
+    if c["op"] == "tree" or c.get("what", "").startswith("append16"):
+        s["k"], s["v"] = k, v
+    else:
+        s["k8"], s["ks"] = _quantised(k)
+        s["v8"], s["vs"] = _quantised(v)
+    if c["op"] == "cache":
+        if c["n"]:
+            # the accepted path of a tree: rows of qkv in ascending order
+            s["rows"] = torch.tensor(sorted(host.sample(range(T), c["n"])), dtype=torch.int32,
+                                     device=dev)
+        if c["what"] == "read8":
+            s["k"], s["v"] = torch.zeros_like(k), torch.zeros_like(v)
+        return s
+    s["mask"] = _tree_words(T, host).to(dev) if c["mask"] == "tree" else None
+    return s
+
+
+# ------------------------------------------------------------------ plain forms
+
+def _angles(s, c):
+    """cos and sin [T, 1, rot / 2]; the angle of a far position needs 64 bits."""
+    pos = s["positions"] if s["positions"] is not None else \
+        c["past"] + torch.arange(c["T"], device=s["qkv"].device)
+    a = pos.double()[:, None] * s["inv_freq"].double()
+    return a.cos().float()[:, None], a.sin().float()[:, None]
+
+
+def _split(x, c):
+    """The two members of each rotated pair."""
+    r = x[..., :c["rot"]]
+    return (r[..., :c["rot"] // 2], r[..., c["rot"] // 2:]) if c["layout"] == "half" else \
+        (r[..., 0::2], r[..., 1::2])
+
+
+def _join(a, b, c):
+    return torch.cat([a, b], -1) if c["layout"] == "half" else torch.stack([a, b], -1).flatten(-2)
+
+
+def _rotate(x, cos, sin, c):
+    a, b = _split(x, c)
+    return torch.cat([_join(a * cos - b * sin, b * cos + a * sin, c), x[..., c["rot"]:]], -1)
+
+
+def _plain_qk(s, c):
+    T, nq, nkv, d = c["T"], c["nq"], c["nkv"], c["d"]
+    x = s["qkv"].float().view(T, nq + 2 * nkv, d)
+    qk, v = x[:, :nq + nkv], x[:, nq + nkv:]
+    if c["norm"]:
+        gamma = torch.cat([s["gamma_q"].float().expand(nq, d), s["gamma_k"].float().expand(nkv, d)])
+        r = torch.rsqrt(qk.square().mean(-1, keepdim=True) + EPS)
+    if not c["back"]:
+        y = qk * r * gamma if c["norm"] else qk
+        if c["rot"]:
+            y = _rotate(y, *_angles(s, c), c)
+        return torch.cat([y, v], 1).reshape(T, -1).to(torch.bfloat16)
+    dy = s["dout"].float().view(T, nq + 2 * nkv, d)
+    dz, dv = dy[:, :nq + nkv], dy[:, nq + nkv:]
+    if c["rot"]:
+        cos, sin = _angles(s, c)
+        dz = _rotate(dz, cos, -sin, c)  # the transpose of a rotation turns the other way
+    dx, dgq, dgk = dz, None, None
+    if c["norm"]:
+        n = qk * r
+        dgq = (dz * n)[:, :nq].sum((0, 1), dtype=torch.float64).to(torch.bfloat16)
+        dgk = (dz * n)[:, nq:].sum((0, 1), dtype=torch.float64).to(torch.bfloat16)
+        gz = dz * gamma
+        dx = r * (gz - n * (gz * n).mean(-1, keepdim=True))
+    return {"dqkv": torch.cat([dx, dv], 1).reshape(T, -1).to(torch.bfloat16),
+            "dgamma_q": dgq, "dgamma_k": dgk}
+
+
+def _new_kv(s, c):
+    """The new tokens' keys and values [nkv, T, d]."""
+    x = s["qkv"].view(c["T"], -1, c["d"])
+    return x[:, c["nq"]:c["nq"] + c["nkv"]].transpose(0, 1), x[:, c["nq"] + c["nkv"]:].transpose(0, 1)
+
+
+def _values(codes, scale):
+    return codes.view(torch.float8_e4m3fn).float() * scale[..., None]
+
+
+def _codes(s):
+    """The 8-bit cache as the values that its codes stand for."""
+    return {"k8": s["k8"].view(torch.float8_e4m3fn), "ks": s["ks"],
+            "v8": s["v8"].view(torch.float8_e4m3fn), "vs": s["vs"]}
+
+
+def _append(s, c, k, v):
+    end = c["past"] + k.shape[1]
+    if "k8" in s:
+        s["k8"][:, c["past"]:end], s["ks"][:, c["past"]:end] = _quantised(k)
+        s["v8"][:, c["past"]:end], s["vs"][:, c["past"]:end] = _quantised(v)
+    else:
+        s["k"][:, c["past"]:end], s["v"][:, c["past"]:end] = k, v
+
+
+def _plain_cache(s, c):
+    if c["what"] == "read8":
+        s["k"][:, :c["past"]] = _values(s["k8"], s["ks"])[:, :c["past"]].to(torch.bfloat16)
+        s["v"][:, :c["past"]] = _values(s["v8"], s["vs"])[:, :c["past"]].to(torch.bfloat16)
+        return [s["k"], s["v"]]
+    k, v = _new_kv(s, c)
+    if c["n"]:
+        k, v = k[:, s["rows"].long()], v[:, s["rows"].long()]
+    _append(s, c, k, v)
+    return _codes(s) if "k8" in s else [s["k"], s["v"]]
+
+
+def _visible(s, c):
+    """[T, past + T]: every cached token, and the new ones that the mask names."""
+    T, dev = c["T"], s["qkv"].device
+    if s["mask"] is None:
+        new = torch.ones(T, T, dtype=torch.bool, device=dev).tril()
+    else:
+        bits = (s["mask"][:, :, None] >> torch.arange(64, device=dev)) & 1
+        new = bits.flatten(1)[:, :T].bool()
+    return torch.cat([torch.ones(T, c["past"], dtype=torch.bool, device=dev), new], 1)
+
+
+def _plain_attn(s, c):
+    T, nq, nkv, d, L = c["T"], c["nq"], c["nkv"], c["d"], c["past"] + c["T"]
+    _append(s, c, *_new_kv(s, c))
+    if "k8" in s:
+        k, v = _values(s["k8"][:, :L], s["ks"][:, :L]), _values(s["v8"][:, :L], s["vs"][:, :L])
+    else:
+        k, v = s["k"][:, :L].float(), s["v"][:, :L].float()
+    q = s["qkv"][:, :nq * d].float().view(T, nkv, nq // nkv, d).permute(1, 0, 2, 3)
+    score = q.reshape(nkv, -1, d) @ k.transpose(1, 2) / math.sqrt(d)
+    hidden = ~_visible(s, c).repeat_interleave(nq // nkv, 0)
+    score = score.masked_fill(hidden, float("-inf"))
+    p = torch.exp(score - score.amax(-1, keepdim=True))
+    ctx = (p @ v) / p.sum(-1, keepdim=True)
+    ctx = ctx.view(nkv, T, nq // nkv, d).permute(1, 0, 2, 3).reshape(T, nq * d).to(torch.bfloat16)
+    return {"ctx": ctx, **(_codes(s) if "k8" in s else {"k": s["k"], "v": s["v"]})}
+
+
+# ------------------------------------------------------------------ the package's calls
+
+def _own(s, c):
+    import tensor_transformer_linear_column_b200 as tp
+    heads = (c["nq"], c["nkv"], c["d"], c["t"])
+    if c["op"] == "qk":
+        common = dict(gamma_q=s["gamma_q"], gamma_k=s["gamma_k"], inv_freq=s["inv_freq"],
+                      positions=s["positions"], layout=c["layout"], eps=EPS)
+        if not c["back"]:
+            return tp.tp_qk_norm_rope(s["qkv"], c["past"], *heads, out=s["out"], **common)
+        return tp.tp_qk_norm_rope_backward(s["qkv"], s["dout"], c["past"], *heads, **common)
+    if c["op"] == "cache":
+        if c["what"] == "read8":
+            tp.tp_kv8_read(s["k8"], s["ks"], s["v8"], s["vs"], 0, c["past"], c["t"],
+                           k_out=s["k"], v_out=s["v"])
+            return [s["k"], s["v"]]
+        if "k8" in s:
+            tp.tp_kv8_append(s["qkv"], s["k8"], s["ks"], s["v8"], s["vs"], c["past"], *heads,
+                             rows=s.get("rows"))
+            return _codes(s)
+        tp.tp_kv_append(s["qkv"], s["k"], s["v"], c["past"], *heads, rows=s.get("rows"))
+        return [s["k"], s["v"]]
+    if c["op"] == "decode_kv8":
+        ctx = tp.tp_attn_decode_kv8(s["qkv"], s["k8"], s["ks"], s["v8"], s["vs"], c["past"],
+                                    *heads, tree_mask=s["mask"])
+        return {"ctx": ctx, **_codes(s)}
+    ctx = tp.tp_attn_tree(s["qkv"], s["k"], s["v"], c["past"], *heads, tree_mask=s["mask"])
+    return {"ctx": ctx, "k": s["k"], "v": s["v"]}
+
+
+def run(state):
+    c = state["case"]
+    if own:
+        return _own(state, c)
+    if c["op"] == "qk":
+        return _plain_qk(state, c)
+    return _plain_cache(state, c) if c["op"] == "cache" else _plain_attn(state, c)
+
+
+def work(case):
+    c = case
+    T, nq, nkv, d, past = c["T"], c["nq"], c["nkv"], c["d"], c["past"]
+    row = (nq + 2 * nkv) * d
+    if c["op"] == "qk":
+        reads = (2 if c["back"] else 1) * T * row * 2 + (4 * T if c["far"] else 0) + 2 * c["rot"]
+        params = 4 * d * (2 if c["back"] else 1) if c["norm"] else 0
+        per = (12 if c["norm"] else 3) * (2 if c["back"] else 1)
+        return {"bytes": reads + T * row * 2 + params, "flops": T * (nq + nkv) * d * per}
+    one8 = 2 * nkv * (d + 4)          # a token's codes and scales
+    one16 = 2 * nkv * d * 2
+    if c["op"] == "cache":
+        n = c["n"] or T
+        if c["what"] == "read8":
+            return {"bytes": past * (one8 + one16), "flops": past * 2 * nkv * d}
+        return {"bytes": n * (one16 + (one8 if c["what"].startswith("append8") else one16)),
+                "flops": n * 2 * nkv * d * 3 if c["what"].startswith("append8") else 0}
+    one = one8 if c["op"] == "decode_kv8" else one16
+    words = 8 * T * ((T + 63) // 64) if c["mask"] == "tree" else 0
+    return {"bytes": T * row * 2 + T * nq * d * 2 + past * one + T * one + words,
+            "flops": 4 * T * nq * d * (past + (T + 1) // 2)}
+
+
+# ------------------------------------------------------------------ the definition in 64 bits
+
+def _exact_qk(s, c):
+    T, nq, nkv, d, rot = c["T"], c["nq"], c["nkv"], c["d"], c["rot"]
+    heads = nq + 2 * nkv
+    x = s["qkv"].double().reshape(T, heads, d)
+    gamma = torch.ones(heads, d, dtype=torch.float64, device=x.device)
+    inv = torch.ones(T, heads, 1, dtype=torch.float64, device=x.device)
+    if c["norm"]:
+        gamma[:nq], gamma[nq:nq + nkv] = s["gamma_q"].double(), s["gamma_k"].double()
+        inv[:, :nq + nkv] = 1 / ((x * x).sum(-1, keepdim=True) / d + EPS).sqrt()[:, :nq + nkv]
+    turn = None
+    if rot:
+        pos = torch.arange(c["past"], c["past"] + T, device=x.device) \
+            if s["positions"] is None else s["positions"]
+        angle = pos.double()[:, None, None] * s["inv_freq"].double()
+        turn = torch.complex(torch.cos(angle), torch.sin(angle))
+    # position in the head of the first and second member of pair i
+    i = torch.arange(rot // 2, device=x.device)
+    first, second = (i, i + rot // 2) if c["layout"] == "half" else (2 * i, 2 * i + 1)
+
+    def spin(y, w):
+        y = y.clone()
+        if rot:
+            z = torch.complex(y[:, :nq + nkv][..., first], y[:, :nq + nkv][..., second]) * w
+            y[:, :nq + nkv, first], y[:, :nq + nkv, second] = z.real, z.imag
+        return y
+
+    if not c["back"]:
+        return spin(x * inv * gamma, turn).reshape(T, -1)
+    dz = spin(s["dout"].double().reshape(T, heads, d), turn.conj() if rot else None)
+    if not c["norm"]:
+        return {"dqkv": dz.reshape(T, -1), "dgamma_q": None, "dgamma_k": None}
+    dx = dz * gamma * inv
+    hit = (dz * gamma * x).sum(-1, keepdim=True) * inv ** 3 / d
+    dx[:, :nq + nkv] -= (x * hit)[:, :nq + nkv]
+    dg = (dz * x * inv).sum(0)
+    return {"dqkv": dx.reshape(T, -1), "dgamma_q": dg[:nq].sum(0), "dgamma_k": dg[nq:nq + nkv].sum(0)}
+
+
+def _exact_codes(x):
+    """Nearest E4M3 values of rows x / scale, and the scales, in 64 bits."""
+    x = x.double()
+    big = x.abs().max(-1).values
+    scale = torch.where(big > 0, big / E4M3_MAX, torch.ones_like(big))
+    y = x / scale.unsqueeze(-1)
+    # the spacing of E4M3 at |y|: 2^(exponent - 3), never below 2^-9
+    step = torch.ldexp(torch.ones_like(y), (torch.frexp(y).exponent - 4).clamp(min=-9))
+    return torch.round(y / step) * step, scale
+
+
+def _e4m3(codes):
+    """Values of E4M3 bytes by their definition."""
+    b = codes.to(torch.int32)
+    e, m = (b >> 3) & 15, (b & 7).double()
+    mag = torch.where(e > 0, torch.ldexp(1 + m / 8, e - 7), torch.ldexp(m, torch.full_like(e, -9)))
+    return torch.where(b >= 128, -mag, mag)
+
+
+def exact(case, seed):
+    c, s = case, prepare(case, seed)
+    T, nq, nkv, d, past = c["T"], c["nq"], c["nkv"], c["d"], c["past"]
+    if c["op"] == "qk":
+        return _exact_qk(s, c)
+    if c["op"] == "cache" and c["what"] == "read8":
+        out = [torch.zeros_like(s["k"], dtype=torch.float64) for _ in range(2)]
+        for o, q, sc in zip(out, (s["k8"], s["v8"]), (s["ks"], s["vs"])):
+            o[:, :past] = _e4m3(q[:, :past]) * sc[:, :past, None].double()
+        return out
+    x = s["qkv"].double().reshape(T, nq + 2 * nkv, d)
+    fresh = [x[:, nq:nq + nkv].permute(1, 0, 2), x[:, nq + nkv:].permute(1, 0, 2)]
+    if c["op"] == "cache" and c["n"]:
+        fresh = [f[:, s["rows"].long()] for f in fresh]
+    eight = "k8" in s
+    state, full = {}, []
+    for name, f in zip("kv", fresh):
+        if eight:
+            q, sc = _e4m3(s[name + "8"]), s[name + "s"].double()
+            q[:, past:past + f.shape[1]], sc[:, past:past + f.shape[1]] = _exact_codes(f)
+            state[name + "8"], state[name + "s"] = q, sc
+            full.append((q, sc))
+        else:
+            m = s[name].double()
+            m[:, past:past + f.shape[1]] = f
+            state[name] = m
+            full.append((m, None))
+    if c["op"] == "cache":
+        return state if eight else [state["k"], state["v"]]
+    G, L = nq // nkv, past + T
+    seen = torch.ones(T, L, dtype=torch.bool, device=x.device)
+    for i in range(T):
+        for j in range(T):
+            if s["mask"] is None:
+                seen[i, past + j] = j <= i
+    if s["mask"] is not None:
+        words = s["mask"].cpu().tolist()
+        seen[:, past:] = torch.tensor([[bool((words[i][j // 64] >> (j % 64)) & 1) for j in range(T)]
+                                       for i in range(T)], device=x.device)
+    ctx = torch.empty(T, nq, d, dtype=torch.float64, device=x.device)
+    for g in range(nkv):
+        kg, vg = ((m[g, :L] * sc[g, :L, None]) if sc is not None else m[g, :L] for m, sc in full)
+        for h in range(g * G, (g + 1) * G):
+            w = torch.softmax((x[:, h] @ kg.T / math.sqrt(d)).masked_fill(~seen, -math.inf), -1)
+            ctx[:, h] = w @ vg
+    return {"ctx": ctx.reshape(T, nq * d), **state}
