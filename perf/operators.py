@@ -120,12 +120,11 @@ def _tree_words(T, rng):
 
 
 def _quantised(x):
-    """8-bit codes (uint8) and fp32 scales of bf16 rows: scale = max |row| / 448,
-    1 for a row of zeros."""
+    """8-bit codes (uint8) and fp32 scales of bf16 rows: scale = max |row| / 448
+    (0 for a row of zeros, whose codes are 0)."""
     xf = x.float()
-    amax = xf.abs().amax(-1)
-    scale = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax))
-    q = (xf / scale[..., None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+    scale = xf.abs().amax(-1) / E4M3_MAX
+    q = (xf / torch.where(scale > 0, scale, 1.0)[..., None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     return q.view(torch.uint8), scale
 
 
@@ -409,8 +408,8 @@ def _exact_codes(x):
     """Nearest E4M3 values of rows x / scale, and the scales, in 64 bits."""
     x = x.double()
     big = x.abs().max(-1).values
-    scale = torch.where(big > 0, big / E4M3_MAX, torch.ones_like(big))
-    y = x / scale.unsqueeze(-1)
+    scale = big / E4M3_MAX
+    y = x / torch.where(big > 0, scale, torch.ones_like(big)).unsqueeze(-1)
     # the spacing of E4M3 at |y|: 2^(exponent - 3), never below 2^-9
     step = torch.ldexp(torch.ones_like(y), (torch.frexp(y).exponent - 4).clamp(min=-9))
     return torch.round(y / step) * step, scale
