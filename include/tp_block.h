@@ -83,6 +83,11 @@ typedef enum tp_act {
   TP_ACT_GELU_TANH = 1        /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))     */
 } tp_act;
 
+typedef enum tp_rope {
+  TP_ROPE_HALF = 0,           /* pair p is elements (p, p + rot_dim / 2)             */
+  TP_ROPE_PAIRS = 1           /* pair p is elements (2 p, 2 p + 1)                   */
+} tp_rope;
+
 /*
  * Column-parallel linear (+ bias, + activation).
  *   out[T, N] = act(x[T, K] @ w[N, K]^T + b[N])
@@ -281,6 +286,178 @@ tp_status tp_attn_decode(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,
 tp_status tp_attn_prefill(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache, int T,
                           int past, int max_len, int n_q_heads, int n_kv_heads, int head_dim,
                           int tp_degree, tp_bf16* ctx, tp_stream_t stream);
+
+/*
+ * RMS norms of queries and keys for each head, with the position rotation in
+ * the same pass: the step between the QKV projection and the attention core.
+ * The attention calls apply neither; a model that wants them runs this call on
+ * tp_attn_proj_forward's qkv_out first.  Shards own whole heads, so nothing is
+ * exchanged.  For each query or key head x of token i, at position t_i:
+ *   z = gamma * x / sqrt(mean_j x_j^2 + eps)     gamma_q for query heads, gamma_k
+ *                                                for key heads; both NULL: z = x
+ *   out = z with pair p of its first rot_dim elements turned by the angle
+ *         t_i * inv_freq[p]; the elements from rot_dim on are z
+ * Value heads pass through.  Arithmetic: fp32 from the bf16 inputs; the angle
+ * and its remainder by 2 pi in 64 bits, so that far positions stay exact; one
+ * rounding to bf16.
+ *   qkv       [T, (nq + 2 nkv) d]                                    (read)
+ *   gamma_q, gamma_k [d] bf16, or both NULL for no norm              (read)
+ *   inv_freq  [rot_dim / 2] fp32; may be NULL if rot_dim is 0        (read)
+ *   positions [T] int32, or NULL: token i is at position past + i    (read)
+ *   layout    a tp_rope value
+ *   out       [T, (nq + 2 nkv) d] (written): another buffer, or qkv itself (the
+ *             one exception to "outputs must not alias inputs"; the value heads
+ *             are then not touched)
+ * Requires d a multiple of 16 up to 256, rot_dim a multiple of 16 in [0, d],
+ * nq a multiple of nkv, eps >= 0 (else TP_ERR_SHAPE); t dividing both head
+ * counts.  One of gamma_q and gamma_k alone is TP_ERR_NULL.
+ */
+tp_status tp_qk_norm_rope(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf16* gamma_k,
+                          const float* inv_freq, const int32_t* positions, int T, int past,
+                          int n_q_heads, int n_kv_heads, int head_dim, int rot_dim, int layout,
+                          float eps, int tp_degree, tp_bf16* out, tp_stream_t stream);
+
+/*
+ * Bytes of workspace tp_qk_norm_rope_backward needs with norms (the blocks'
+ * shares of the gains' gradients); it needs none without.  0 for sizes out of
+ * range.
+ */
+size_t tp_qk_norm_rope_backward_workspace_bytes(int T, int head_dim);
+
+/*
+ * Gradients of tp_qk_norm_rope for an upstream gradient dout of its result.
+ * With x a head of qkv, r = 1 / sqrt(mean_j x_j^2 + eps) and dz = dout turned
+ * back by the token's angles:
+ *   dgamma = sum over tokens and heads of dz * x r      (queries, keys)
+ *   dx     = r gamma dz - x r^3 / d * sum_j gamma_j dz_j x_j
+ * The value heads' gradient is dout's.  Arithmetic: fp32; dgamma is summed in
+ * fp32 in a fixed order; every output is rounded once to bf16.
+ *   qkv   the forward call's input (not its result), dout [T, (nq + 2 nkv) d]
+ *   dqkv  [T, (nq + 2 nkv) d] (written): another buffer, or dout itself
+ *   dgamma_q, dgamma_k [d] (written; not used without norms)
+ *   workspace: at least tp_qk_norm_rope_backward_workspace_bytes(T, d) bytes,
+ *   16-byte aligned (not used without norms)
+ * Other arguments and checks as tp_qk_norm_rope.
+ */
+tp_status tp_qk_norm_rope_backward(const tp_bf16* qkv, const tp_bf16* gamma_q,
+                                   const tp_bf16* gamma_k, const float* inv_freq,
+                                   const int32_t* positions, const tp_bf16* dout, int T, int past,
+                                   int n_q_heads, int n_kv_heads, int head_dim, int rot_dim,
+                                   int layout, float eps, int tp_degree, tp_bf16* dqkv,
+                                   tp_bf16* dgamma_q, tp_bf16* dgamma_k, void* workspace,
+                                   size_t workspace_bytes, tp_stream_t stream);
+
+/*
+ * Keys and values of new tokens into a bf16 cache: row j of n goes to cache row
+ * past + j of every key-value head, copied from the K and V columns of row
+ * rows[j] of qkv (rows NULL: row j; then n <= T).  With rows, this keeps the
+ * accepted path of a drafted tree: after tp_attn_tree has written all T tokens
+ * behind the cache, appending the accepted ones again at the same `past`
+ * leaves them in order.  A row index outside [0, T) leaves its cache row as it
+ * was; an index may occur more than once.
+ *   qkv [T, (nq + 2 nkv) d], rows [n] int32 or NULL              (read)
+ *   k_cache, v_cache [nkv, max_len, d]: rows [past, past + n)    (written)
+ * Requires d a multiple of 16 up to 256, nq a multiple of nkv, n >= 1 and
+ * past + n <= max_len (else TP_ERR_SHAPE); t dividing both head counts.
+ */
+tp_status tp_kv_append(const tp_bf16* qkv, const int32_t* rows, tp_bf16* k_cache, tp_bf16* v_cache,
+                       int T, int n, int past, int max_len, int n_q_heads, int n_kv_heads,
+                       int head_dim, int tp_degree, tp_stream_t stream);
+
+/*
+ * The same into an 8-bit cache: half the bytes that every later token reads.
+ * A row (one token, one key-value head, K or V) is d E4M3 codes (the encoding
+ * of the *_w8 calls) and one fp32 scale, and stands for scale * code:
+ *   scale = max_j |x_j| / 448
+ *   code_j = E4M3(x_j / scale), nearest, ties to even, at most 448 in magnitude
+ * Both divisions are IEEE fp32; a row of zeros has scale 0 and zero codes.  A NaN element is not counted in the maximum
+ * and becomes the NaN code; a row with an infinity reads back as NaN.
+ *   k_cache, v_cache [nkv, max_len, d] bytes; k_scale, v_scale [nkv, max_len]
+ */
+tp_status tp_kv8_append(const tp_bf16* qkv, const int32_t* rows, uint8_t* k_cache, float* k_scale,
+                        uint8_t* v_cache, float* v_scale, int T, int n, int past, int max_len,
+                        int n_q_heads, int n_kv_heads, int head_dim, int tp_degree,
+                        tp_stream_t stream);
+
+/*
+ * Rows [start, start + count) of an 8-bit cache as bf16, scale * code rounded
+ * once, into the same rows of bf16 caches [nkv, out_len, d] -- for example the
+ * cached tokens before tp_attn_prefill takes the next chunk of a long prompt.
+ * Rows outside the range are not touched.
+ * Requires count >= 1, start + count <= max_len and <= out_len, d a multiple
+ * of 16 up to 256 (else TP_ERR_SHAPE), t dividing nkv.
+ */
+tp_status tp_kv8_read(const uint8_t* k_cache, const float* k_scale, const uint8_t* v_cache,
+                      const float* v_scale, int start, int count, int max_len, int n_kv_heads,
+                      int head_dim, int tp_degree, tp_bf16* k_out, tp_bf16* v_out, int out_len,
+                      tp_stream_t stream);
+
+/*
+ * Visibility words of a drafted tree, host arithmetic on host memory: token i's
+ * parent is parents[i] < i, or -1 for a token that follows the cached ones
+ * directly; bit j % 64 of mask[i * ceil(T / 64) + j / 64] is set for j = i and
+ * for every ancestor j of i.  TP_ERR_SHAPE for T outside [1, 128] or a parent
+ * outside [-1, i).
+ */
+tp_status tp_tree_mask(const int32_t* parents, int T, uint64_t* mask);
+
+/*
+ * Bytes of workspace that tp_attn_tree and tp_attn_decode_kv8 need for T new
+ * tokens after `past` cached ones; 0 for past = 0 and for unsupported
+ * arguments.  A function of the sizes only.
+ */
+size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads, int head_dim);
+
+/*
+ * Attention of a tree of drafted tokens over a cache: tp_attn_decode with a
+ * mask among the new tokens, so that one pass scores every branch.
+ *   1. the new tokens' keys and values (columns K and V of qkv) are written
+ *      into the cache at positions [past, past + T), in the order of qkv;
+ *   2. ctx[i, h d .. h d + d) = sum_j p_j v_j over the cached keys j < past and
+ *      the new keys past + j whose bit j of row i of tree_mask is set, with
+ *      p = softmax_j(q_i,h . k_j / sqrt(d)); tree_mask NULL: j <= i.
+ * Any bit may be set or clear; bits at or above T are not read.  A row that
+ * sees nothing (past = 0, no bit set) is zero.  The key and value of a new
+ * token reach only the rows that see it, NaN and infinities included.
+ * Arithmetic: bf16 q, k, v; scores, maxima and sums in fp32; over the cached
+ * keys the softmax weights are rounded to bf16 for the weighted sum of v (fp32
+ * accumulate) and lie in [0, 2^4] before normalisation (the running maximum is
+ * raised only when a block of 128 keys exceeds it by more than that), over the
+ * new ones they stay fp32.  Every order is fixed: results are bit-identical
+ * from run to run.
+ *   qkv       [T, (nq + 2 nkv) d]; tree_mask [T, ceil(T / 64)] words or NULL
+ *   k_cache, v_cache [nkv, max_len, d]: rows [0, past) are read, rows
+ *             [past, past + T) written
+ *   ctx       [T, nq d]                                            (written)
+ *   workspace: at least tp_attn_tree_workspace_bytes(...) bytes, 16-byte
+ *   aligned; may be NULL if that is 0; contents on return unspecified.
+ * Requires T <= 128, head_dim == 128 and nq / nkv <= 16 (else
+ * TP_ERR_UNSUPPORTED), nq a multiple of nkv, past + T <= max_len (else
+ * TP_ERR_SHAPE), and t dividing both head counts.  Calls that overlap on the
+ * GPU must not share a workspace or a cache.
+ */
+tp_status tp_attn_tree(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,
+                       const uint64_t* tree_mask, int T, int past, int max_len, int n_q_heads,
+                       int n_kv_heads, int head_dim, int tp_degree, tp_bf16* ctx, void* workspace,
+                       size_t workspace_bytes, tp_stream_t stream);
+
+/*
+ * The same attention over an 8-bit cache (see tp_kv8_append): decode with
+ * tree_mask NULL, or a drafted tree.  The new tokens' keys and values are
+ * written as codes and scales, and what is attended to is scale * code, the
+ * new tokens' own included.  The codes meet the tensor cores as they are:
+ * queries are split into two E4M3 terms (exact for elements of at least 2^-9
+ * of their head's largest, within 2^-17 of the largest below that), softmax
+ * weights times the values' scales into three E5M2 terms (relative error
+ * 2^-9, or 2^-28 of the largest weight times the largest value scale of a
+ * chunk of the cache).  A query head that holds an infinity gives NaN.  Other
+ * arguments, checks and errors as tp_attn_tree.
+ */
+tp_status tp_attn_decode_kv8(const tp_bf16* qkv, uint8_t* k_cache, float* k_scale, uint8_t* v_cache,
+                             float* v_scale, const uint64_t* tree_mask, int T, int past,
+                             int max_len, int n_q_heads, int n_kv_heads, int head_dim,
+                             int tp_degree, tp_bf16* ctx, void* workspace, size_t workspace_bytes,
+                             tp_stream_t stream);
 
 /*
  * The sequence-parallel region after a row-parallel linear: residual add and

@@ -32,3 +32,12 @@ from .tp_sequence import (  # noqa: F401
     sp_residual_norm,
     token_shards,
 )
+from .tp_serving import (  # noqa: F401
+    attn_masked,
+    e4m3_codes,
+    kv8_quantize,
+    kv8_values,
+    qk_norm_rope,
+    qk_norm_rope_backward,
+    tree_visible,
+)

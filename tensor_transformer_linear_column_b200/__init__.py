@@ -29,15 +29,20 @@ TP_ERR_DEVICE_TIMEOUT = 8
 TP_ACT_NONE = 0
 TP_ACT_GELU_TANH = 1
 
+TP_ROPE_HALF = 0
+TP_ROPE_PAIRS = 1
+
 TP_OPT_PDL = 1
 TP_OPT_STATIC_WEIGHTS = 2
 
 ACTS = {"none": TP_ACT_NONE, "gelu_tanh": TP_ACT_GELU_TANH}
+ROPE_LAYOUTS = {"half": TP_ROPE_HALF, "pairs": TP_ROPE_PAIRS}
 
 # name -> (restype, argtypes) of every symbol declared in include/tp_block.h
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
+_F = ctypes.c_float
 SIGNATURES = {
     "tp_colpar_gemm_gelu": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "tp_rowpar_gemm_reduce": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
@@ -50,6 +55,18 @@ SIGNATURES = {
     "tp_sp_add_rmsnorm": (_I, [_P, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, _P]),
     "tp_attn_decode": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z, _P]),
     "tp_attn_prefill": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "tp_qk_norm_rope": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P]),
+    "tp_qk_norm_rope_backward_workspace_bytes": (_Z, [_I, _I]),
+    "tp_qk_norm_rope_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                                      _P, _P, _P, _P, _Z, _P]),
+    "tp_kv_append": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "tp_kv8_append": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "tp_kv8_read": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P]),
+    "tp_tree_mask": (_I, [_P, _I, _P]),
+    "tp_attn_tree_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
+    "tp_attn_tree": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z, _P]),
+    "tp_attn_decode_kv8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z,
+                                _P]),
     "tp_mlp_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _Z,
                              _P]),
     "tp_colpar_gemm_gelu_w8": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
@@ -481,6 +498,274 @@ def tp_sp_add_rmsnorm(y: torch.Tensor, residual: torch.Tensor, gamma: torch.Tens
                                   _stream(stream))
     _check(st, "tp_sp_add_rmsnorm")
     return r_out, n_out
+
+
+def _empty_on(shape, dtype: torch.dtype, dev: torch.device,
+              stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """An uninitialised tensor whose memory belongs to the call's stream: it is
+    handed out again only after the work enqueued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, dev: torch.device,
+               stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    if workspace is None:
+        return _empty_on((max(need, 256),), torch.uint8, dev, stream)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    return workspace
+
+
+def _expect_shape(t: Optional[torch.Tensor], name: str, shape) -> None:
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _qk_args(qkv, gamma_q, gamma_k, inv_freq, positions, n_q_heads, n_kv_heads, head_dim, dev):
+    """Shape checks shared by tp_qk_norm_rope and its gradient; the pointers of
+    the gains, the frequencies and the positions, and rot_dim."""
+    if qkv.dim() != 2 or qkv.shape[1] != (n_q_heads + 2 * n_kv_heads) * head_dim:
+        raise ValueError("qkv must be [T, (nq + 2 nkv) d]")
+    _expect_shape(gamma_q, "gamma_q", (head_dim,))
+    _expect_shape(gamma_k, "gamma_k", (head_dim,))
+    _expect_shape(positions, "positions", (qkv.shape[0],))
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    return (_ptr(gamma_q, "gamma_q", dev), _ptr(gamma_k, "gamma_k", dev),
+            _ptr_typed(inv_freq, "inv_freq", dev, torch.float32) if rot else None,
+            _ptr_typed(positions, "positions", dev, torch.int32), rot)
+
+
+def _layout(layout) -> int:
+    return ROPE_LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+
+
+def tp_qk_norm_rope(qkv: torch.Tensor, past: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                    tp_degree: int, gamma_q: Optional[torch.Tensor] = None,
+                    gamma_k: Optional[torch.Tensor] = None,
+                    inv_freq: Optional[torch.Tensor] = None,
+                    positions: Optional[torch.Tensor] = None, layout="half", eps: float = 1e-5,
+                    out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """RMS norm of every query and key head (gamma_q, gamma_k [d], or neither) and
+    the rotation of its first 2 len(inv_freq) elements by position * inv_freq:
+    qkv [T, (nq + 2 nkv) d] to a buffer of the same shape, which may be qkv
+    itself (out=qkv).  Token i is at positions[i] (int32), or at past + i;
+    layout "half" pairs (p, p + rot / 2), "pairs" (2 p, 2 p + 1)."""
+    dev = _device(qkv)
+    gq, gk, fr, pos, rot = _qk_args(qkv, gamma_q, gamma_k, inv_freq, positions, n_q_heads,
+                                    n_kv_heads, head_dim, dev)
+    if out is None:
+        out = _empty_on(tuple(qkv.shape), torch.bfloat16, dev, stream)
+    _expect_shape(out, "out", qkv.shape)
+    st = load().tp_qk_norm_rope(_ptr(qkv, "qkv", dev), gq, gk, fr, pos, qkv.shape[0], int(past),
+                                int(n_q_heads), int(n_kv_heads), int(head_dim), rot,
+                                _layout(layout), float(eps), int(tp_degree),
+                                _ptr(out, "out", dev), _stream(stream))
+    _check(st, "tp_qk_norm_rope")
+    return out
+
+
+def tp_qk_norm_rope_backward_workspace_bytes(T: int, head_dim: int) -> int:
+    return int(load().tp_qk_norm_rope_backward_workspace_bytes(int(T), int(head_dim)))
+
+
+def tp_qk_norm_rope_backward(qkv: torch.Tensor, dout: torch.Tensor, past: int, n_q_heads: int,
+                             n_kv_heads: int, head_dim: int, tp_degree: int,
+                             gamma_q: Optional[torch.Tensor] = None,
+                             gamma_k: Optional[torch.Tensor] = None,
+                             inv_freq: Optional[torch.Tensor] = None,
+                             positions: Optional[torch.Tensor] = None, layout="half",
+                             eps: float = 1e-5, dqkv: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of tp_qk_norm_rope for the upstream gradient dout of its result:
+    {"dqkv", "dgamma_q", "dgamma_k"} (the gains' None without norms).  qkv is the
+    forward call's input, so a forward call that is to be differentiated must not
+    run in place; dqkv may be dout itself."""
+    dev = _device(qkv)
+    gq, gk, fr, pos, rot = _qk_args(qkv, gamma_q, gamma_k, inv_freq, positions, n_q_heads,
+                                    n_kv_heads, head_dim, dev)
+    _expect_shape(dout, "dout", qkv.shape)
+    T = qkv.shape[0]
+    if dqkv is None:
+        dqkv = _empty_on(tuple(qkv.shape), torch.bfloat16, dev, stream)
+    _expect_shape(dqkv, "dqkv", qkv.shape)
+    dgq = dgk = ws = None
+    if gq is not None:
+        dgq = _empty_on((head_dim,), torch.bfloat16, dev, stream)
+        dgk = _empty_on((head_dim,), torch.bfloat16, dev, stream)
+        ws = _workspace(workspace, tp_qk_norm_rope_backward_workspace_bytes(T, head_dim), dev,
+                        stream)
+    st = load().tp_qk_norm_rope_backward(
+        _ptr(qkv, "qkv", dev), gq, gk, fr, pos, _ptr(dout, "dout", dev), T, int(past),
+        int(n_q_heads), int(n_kv_heads), int(head_dim), rot, _layout(layout), float(eps),
+        int(tp_degree), _ptr(dqkv, "dqkv", dev), _ptr(dgq, "dgamma_q", dev),
+        _ptr(dgk, "dgamma_k", dev), None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, "tp_qk_norm_rope_backward")
+    return {"dqkv": dqkv, "dgamma_q": dgq, "dgamma_k": dgk}
+
+
+def _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim) -> None:
+    if qkv.dim() != 2 or qkv.shape[1] != (n_q_heads + 2 * n_kv_heads) * head_dim:
+        raise ValueError("qkv must be [T, (nq + 2 nkv) d]")
+    if k_cache.dim() != 3 or tuple(k_cache.shape) != tuple(v_cache.shape) or \
+            k_cache.shape[0] != n_kv_heads or k_cache.shape[2] != head_dim:
+        raise ValueError("caches must be [nkv, max_len, d]")
+
+
+def _kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev):
+    _expect_shape(k_scale, "k_scale", k_cache.shape[:2])
+    _expect_shape(v_scale, "v_scale", v_cache.shape[:2])
+    return (_ptr_typed(k_cache, "k_cache", dev, torch.uint8),
+            _ptr_typed(k_scale, "k_scale", dev, torch.float32),
+            _ptr_typed(v_cache, "v_cache", dev, torch.uint8),
+            _ptr_typed(v_scale, "v_scale", dev, torch.float32))
+
+
+def _rows(rows, T, dev):
+    """(pointer, count) of the rows to append; all T without a list."""
+    if rows is None:
+        return None, T
+    if rows.dim() != 1:
+        raise ValueError("rows must be [n]")
+    return _ptr_typed(rows, "rows", dev, torch.int32), rows.shape[0]
+
+
+def tp_kv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, past: int,
+                 n_q_heads: int, n_kv_heads: int, head_dim: int, tp_degree: int,
+                 rows: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Write the keys and values of qkv's rows (int32 `rows` in that order, or all
+    T) into the bf16 caches [nkv, max_len, d] from row `past` on, in place."""
+    _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    dev = _device(qkv)
+    rp, n = _rows(rows, qkv.shape[0], dev)
+    _check(load().tp_kv_append(_ptr(qkv, "qkv", dev), rp, _ptr(k_cache, "k_cache", dev),
+                               _ptr(v_cache, "v_cache", dev), qkv.shape[0], n, int(past),
+                               k_cache.shape[1], int(n_q_heads), int(n_kv_heads), int(head_dim),
+                               int(tp_degree), _stream(stream)), "tp_kv_append")
+
+
+def tp_kv8_append(qkv: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
+                  v_cache: torch.Tensor, v_scale: torch.Tensor, past: int, n_q_heads: int,
+                  n_kv_heads: int, head_dim: int, tp_degree: int,
+                  rows: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> None:
+    """tp_kv_append into an 8-bit cache: E4M3 codes (uint8) [nkv, max_len, d] and
+    fp32 scales [nkv, max_len], a row being scale * e4m3(code)."""
+    _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    dev = _device(qkv)
+    rp, n = _rows(rows, qkv.shape[0], dev)
+    _check(load().tp_kv8_append(_ptr(qkv, "qkv", dev), rp,
+                                *_kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev), qkv.shape[0],
+                                n, int(past), k_cache.shape[1], int(n_q_heads), int(n_kv_heads),
+                                int(head_dim), int(tp_degree), _stream(stream)), "tp_kv8_append")
+
+
+def tp_kv8_read(k_cache: torch.Tensor, k_scale: torch.Tensor, v_cache: torch.Tensor,
+                v_scale: torch.Tensor, start: int, count: int, tp_degree: int,
+                k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None):
+    """(k, v): rows [start, start + count) of an 8-bit cache as bf16 in the same
+    rows of bf16 caches [nkv, out_len, d]; caches that are made here have
+    out_len = start + count, their rows before `start` unset."""
+    if k_cache.dim() != 3 or tuple(k_cache.shape) != tuple(v_cache.shape):
+        raise ValueError("caches must be [nkv, max_len, d]")
+    dev = _device(k_cache)
+    nkv, max_len, d = k_cache.shape
+    shape = tuple((k_out if k_out is not None else v_out).shape) \
+        if k_out is not None or v_out is not None else (nkv, max(int(start) + int(count), 1), d)
+    if len(shape) != 3 or (shape[0], shape[2]) != (nkv, d):
+        raise ValueError("k_out and v_out must be [nkv, out_len, d]")
+    if k_out is None:
+        k_out = _empty_on(shape, torch.bfloat16, dev, stream)
+    if v_out is None:
+        v_out = _empty_on(shape, torch.bfloat16, dev, stream)
+    _expect_shape(v_out, "v_out", k_out.shape)
+    _check(load().tp_kv8_read(*_kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev), int(start),
+                              int(count), max_len, nkv, d, int(tp_degree),
+                              _ptr(k_out, "k_out", dev), _ptr(v_out, "v_out", dev), shape[1],
+                              _stream(stream)), "tp_kv8_read")
+    return k_out, v_out
+
+
+def tp_tree_mask(parents) -> torch.Tensor:
+    """Visibility words of a drafted tree, int64 [T, ceil(T / 64)] on the host:
+    token i sees itself and its ancestors; parents[i] < i is the parent of token
+    i, or -1 (host arithmetic, no GPU needed)."""
+    parents = [int(v) for v in parents]
+    T = len(parents)
+    words = torch.zeros((max(T, 1), max((T + 63) // 64, 1)), dtype=torch.int64)
+    host = (ctypes.c_int32 * max(T, 1))(*parents)
+    _check(load().tp_tree_mask(ctypes.addressof(host), T, words.data_ptr()), "tp_tree_mask")
+    return words
+
+
+def tp_attn_tree_workspace_bytes(T: int, past: int, n_q_heads: int, n_kv_heads: int,
+                                 head_dim: int) -> int:
+    return int(load().tp_attn_tree_workspace_bytes(int(T), int(past), int(n_q_heads),
+                                                   int(n_kv_heads), int(head_dim)))
+
+
+def _tree_call(name, qkv, cache_ptrs, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree,
+               tree_mask, ctx, workspace, stream, dev) -> torch.Tensor:
+    T = qkv.shape[0]
+    _expect_shape(tree_mask, "tree_mask", (T, (T + 63) // 64))
+    if ctx is None:
+        ctx = _empty_on((T, n_q_heads * head_dim), torch.bfloat16, dev, stream)
+    _expect_shape(ctx, "ctx", (T, n_q_heads * head_dim))
+    workspace = _workspace(
+        workspace, tp_attn_tree_workspace_bytes(T, past, n_q_heads, n_kv_heads, head_dim), dev,
+        stream)
+    st = getattr(load(), name)(
+        _ptr(qkv, "qkv", dev), *cache_ptrs, _ptr_typed(tree_mask, "tree_mask", dev, torch.int64), T,
+        int(past), max_len, int(n_q_heads), int(n_kv_heads), int(head_dim), int(tp_degree),
+        _ptr(ctx, "ctx", dev), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    _check(st, name)
+    return ctx
+
+
+def tp_attn_tree(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, past: int,
+                 n_q_heads: int, n_kv_heads: int, head_dim: int, tp_degree: int,
+                 tree_mask: Optional[torch.Tensor] = None, ctx: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """ctx [T, nq d] of T drafted tokens (T <= 128) over bf16 caches
+    [nkv, max_len, d] that hold `past` tokens: every token sees those, and the
+    new tokens that its row of tree_mask names (int64 words on the GPU, see
+    tp_tree_mask; None: causal).  Writes the new tokens' keys and values behind
+    the cached ones, in place."""
+    _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    dev = _device(qkv)
+    return _tree_call("tp_attn_tree", qkv,
+                      (_ptr(k_cache, "k_cache", dev), _ptr(v_cache, "v_cache", dev)),
+                      k_cache.shape[1], past, n_q_heads, n_kv_heads, head_dim, tp_degree,
+                      tree_mask, ctx, workspace, stream, dev)
+
+
+def tp_attn_decode_kv8(qkv: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
+                       v_cache: torch.Tensor, v_scale: torch.Tensor, past: int, n_q_heads: int,
+                       n_kv_heads: int, head_dim: int, tp_degree: int,
+                       tree_mask: Optional[torch.Tensor] = None,
+                       ctx: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """tp_attn_tree over an 8-bit cache (codes uint8 [nkv, max_len, d], scales
+    fp32 [nkv, max_len]); decode when tree_mask is None.  The new tokens are
+    quantised as they are written, and attended to as written."""
+    _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    dev = _device(qkv)
+    return _tree_call("tp_attn_decode_kv8", qkv,
+                      _kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev), k_cache.shape[1], past,
+                      n_q_heads, n_kv_heads, head_dim, tp_degree, tree_mask, ctx, workspace,
+                      stream, dev)
 
 
 def tp_device_error_check() -> int:

@@ -1,0 +1,920 @@
+// attn_tree_kernel.cuh -- attention of the T new tokens of one sequence (a
+// decoded token, a short chunk, or a tree of drafted tokens) over its
+// key-value cache, held in bf16 or in 8 bits.
+//
+// New token i sees every cached key and the new keys j that bit j of row i of
+// `mask` names (no mask: j <= i).  Query head h reads key-value head
+// g = h / G, G = nq / nkv; scores are q . k / sqrt(d).  The work is cut where
+// the mask begins:
+//   attn_tree_kernel        block (chunk c, key-value head g, row group z): the
+//                           cached keys of chunk c, which no mask touches,
+//                           against kRows of the T G query rows of head g;
+//                           writes a partial (maximum, sum, weighted sum of
+//                           values).  The blocks also write the new tokens'
+//                           keys and values behind the cached ones, where no
+//                           block reads in this launch
+//   attn_tree_merge_kernel  per (token, query head): the chunks' partials and
+//                           the visible new tokens, one by one, in a fixed
+//                           order.  A hidden token's key and value are not
+//                           read, so a NaN or an infinity in them reaches no
+//                           row that does not see it; a row that sees nothing
+//                           is zero
+//
+// attn_tree_kernel, per key block b of 128 (16 KB shared-memory stages loaded by
+// TMA in the order K_0, K_1, V_0, K_2, V_1, ...):
+//   S_b^T[key, n] = K_b Q^T       tcgen05.mma, keys as M (a TMEM lane is a key),
+//                                 query rows as N, into one of two TMEM slots
+//   softmax                       one key per thread: its scores against the
+//                                 running maximum m_n of each row; weights
+//                                 p = 2^(s - m) into one of two shared slots
+//   O^T[d, n] += V_b^T P_b^T      tcgen05.mma, d as M, V read as it lies
+// The running maximum is raised only when some weight of the block would exceed
+// 2^4 (kLazyLog2): one vote per block in the usual case, and a
+// reduction over the block's lanes and a rescale of O in the rare one.
+// Weights are stored with the query rows contiguous (an MN-major B operand), so
+// a thread writes its key's weights as 16-byte vectors, without shuffles.
+//
+// 8-bit cache.  The codes go to the tensor cores as they are (kind::f8f6f4),
+// converted nowhere; the operands they meet are split instead, exactly:
+//   - a bf16 query element has 8 significant bits, E4M3 has 4: the element is
+//     scaled by a power of two that brings its row's largest to (224, 448] and
+//     becomes hi + lo, both E4M3.  The sum is exact for elements of at least
+//     2^-9 of the row's largest and within 2^-17 of the largest below that
+//   - a weight p is multiplied by its key's value scale over C, a power of two
+//     at or above every value scale seen so far (a running maximum, raised like
+//     m), and becomes the sum of three E5M2 terms of 3 bits each: relative
+//     error 2^-9, as a bf16 weight has, down to 2^-19 of the largest possible
+//     product, and absolute error at most 2^-28 of it below.  E5M2 is the upper byte of
+//     fp16, so the split is masks and exact subtractions in fp16 pairs
+// Keys' scales multiply the scores, one per lane.  Two score and three value
+// products at the 8-bit rate cost what bf16's one and one cost times 5/4, and
+// nothing is converted.  Sums of weights are of the unrounded ones, in fp32.
+#pragma once
+
+#include "attn_kernel.cuh"
+#include "kv_cache_kernel.cuh"
+#include "rows_bf16.cuh"
+
+namespace tpb {
+
+constexpr int kTreeMaxTokens = 128;
+constexpr int kTreeStageBytes = 16384;  // one TMA item: 128 x 128 codes, or 16 KB of bf16
+constexpr int kTreeMaxStages = 8;
+constexpr float kLazyLog2 = 4.0f;
+constexpr float kUnsetMax = -1e30f;     // the running maximum before the first key
+constexpr int kWeightShift = 11;        // 8 bits: weights are split after times 2^11
+
+struct TreeParams {
+  int T, past, nq, nkv, G;
+  int R;            // query rows per key-value head: T G
+  int groups;       // row groups of kRows: grid z
+  int nblk;         // key blocks of 128 in [0, past)
+  int nb, chunks;   // key blocks per chunk, chunks per key-value head: grid x
+  int max_len;
+  float scale_log2; // log2(e) / sqrt(d)
+  const uint16_t* qkv;       // [T, (nq + 2 nkv) d]
+  void* cache[2];            // K, V [nkv, max_len, d]: bf16 or E4M3 codes
+  float* cache_scale[2];     // [nkv, max_len] (8 bits)
+  float* part_o;             // [groups][nkv][chunks][kRows][d]
+  float* part_ml;            // [groups][nkv][chunks][kRows][2]
+};
+
+template <int kRows, bool k8>
+struct TreeShape {
+  static constexpr int kGroups = kRows >= 32 ? 2 : 1;      // softmax warpgroups
+  static constexpr int kCols = kRows / kGroups;            // query rows per thread
+  static constexpr int kThreads = 64 + 128 * kGroups;      // + TMA warp, MMA warp
+  static constexpr int kBlocksPerSm = kRows <= 32 ? 2 : 1;
+  static constexpr int kKItems = k8 ? 1 : 2;               // stages per K (and per V) block
+  static constexpr int kParts = k8 ? 3 : 1;                // weight operands
+  static constexpr int kPartBytes = 128 * kRows * (k8 ? 1 : 2);
+  static constexpr int kSlotBytes = kParts * kPartBytes;
+  static constexpr int kQBytes = 2 * kRows * 128;          // hi, lo; or the two d halves
+  static constexpr int kTmemCols = kRows == 16 ? 64 : kRows == 32 ? 128 : kRows == 64 ? 256 : 512;
+  static constexpr int kSmallBytes = (4 * kRows + 4 * kRows) * 4 + 32 + 256;
+  static constexpr int kSmemTarget = kBlocksPerSm == 2 ? (228 * 1024) / 2 - 1024 : 227 * 1024;
+  static constexpr int kFit = (kSmemTarget - 1024 - kSmallBytes - kQBytes - 2 * kSlotBytes) /
+                              kTreeStageBytes;
+  static constexpr int kStages = kFit > kTreeMaxStages ? kTreeMaxStages : kFit;
+  static constexpr int kSmem = 1024 + kStages * kTreeStageBytes + kQBytes + 2 * kSlotBytes +
+                               kSmallBytes;
+  static_assert(kStages >= 4, "K, K, V and the next K in flight");
+};
+
+// Descriptor of an MN-major operand without swizzling: 16-byte vectors along MN,
+// 8 consecutive K indices 16 bytes apart (a 128-byte core matrix), core matrices
+// along K `lbo` bytes and along MN `sbo` bytes apart.
+__device__ __forceinline__ uint64_t desc_mnmajor_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  return d;
+}
+
+// Instruction descriptor, kind::f8f6f4: E4M3 A, fp32 D; B is E4M3 or E5M2.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool b_e5m2, bool a_mn,
+                                                    bool b_mn) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 8-bit operands, one M x N x 32 step.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Whether `pred` holds in any thread of the `nthreads` at barrier `id`.
+__device__ __forceinline__ bool named_barrier_any(uint32_t id, uint32_t nthreads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"(static_cast<uint32_t>(pred))
+      : "memory");
+  return r != 0;
+}
+
+// Smallest e with 2^e >= s, within [-100, 120] (0 and negative s: -100).
+__device__ __forceinline__ int scale_exponent(float s) {
+  const uint32_t bits = __float_as_uint(s);
+  const int e = static_cast<int>((bits >> 23) & 0xFFu) - 127 + ((bits & 0x7FFFFFu) != 0 ? 1 : 0);
+  return s > 0.0f ? (e < -100 ? -100 : (e > 120 ? 120 : e)) : -100;
+}
+
+__device__ __forceinline__ float pow2i(int e) {  // -126 <= e <= 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Query rows [row0, row0 + kRows) of head g into shared memory as the K-major B
+// operand, by the softmax threads (16 lanes a row): bf16 as two 64-wide
+// halves, or the 8-bit hi / lo parts with each row's factor in rf_s.  Rows at
+// or past R are zero.
+template <int kRows, bool k8>
+__device__ __forceinline__ void load_queries(const TreeParams& p, int g, int row0, uint8_t* qs,
+                                             float* rf_s, int st, int nthreads) {
+  const int l = st & 15;
+  for (int r = st >> 4; r < kRows; r += nthreads >> 4) {
+    const int rr = row0 + r;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (rr < p.R) {
+      const int tok = rr / p.G, h = g * p.G + rr % p.G;
+      raw = __ldg(reinterpret_cast<const uint4*>(
+                      p.qkv + (static_cast<size_t>(tok) * (p.nq + 2 * p.nkv) + h) * kAttnHeadDim) +
+                  l);
+    }
+    if constexpr (!k8) {
+      // half l / 8, 16-byte chunk l % 8 of the 128-byte row, swizzled
+      *reinterpret_cast<uint4*>(qs + (l >> 3) * (kRows * 128) + r * 128 +
+                                (((l & 7) ^ (r & 7)) << 4)) = raw;
+    } else {
+      float x[8];
+      unpack8(raw, x);
+      float amax = abs_max8(x);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      // shift: amax 2^shift in (224, 448]
+      const uint32_t bits = __float_as_uint(amax);
+      int shift = 8 - (static_cast<int>(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+      shift = amax > 0.0f ? (shift > 126 ? 126 : shift) : 0;
+      const float up = pow2i(shift);  // at least -120
+      float hi_f[8];
+      uint2 hi, lo;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] *= up;
+      hi = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = k < 2 ? hi.x : hi.y;
+        const __half2 h2(__nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>(w >> (16 * (k & 1))), __NV_E4M3));
+        const float2 f = __half22float2(h2);
+        hi_f[2 * k] = f.x;
+        hi_f[2 * k + 1] = f.y;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] -= hi_f[k];  // exact: the low bits of x
+      lo = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+      const int off = r * 128 + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8;
+      *reinterpret_cast<uint2*>(qs + off) = hi;
+      *reinterpret_cast<uint2*>(qs + kRows * 128 + off) = lo;
+      // a row that holds an infinity scores NaN (its parts are clamped)
+      if (l == 0)
+        rf_s[r] = amax > 3.3895314e38f ? __int_as_float(0x7fc00000)
+                                       : p.scale_log2 * pow2i(-shift);
+    }
+  }
+}
+
+// The new tokens' K and V rows of head g behind the cached ones, the rows dealt
+// out over the head's blocks (block index `part` of `parts`), 16 lanes a row.
+template <bool k8>
+__device__ __forceinline__ void append_rows(const TreeParams& p, int g, int part, int parts, int st,
+                                            int nthreads) {
+  const int l = st & 15;
+  const int per_pass = nthreads >> 4;
+  for (int base = 0; base < 2 * p.T; base += parts * per_pass) {
+    const int item = base + (st >> 4) * parts + part;  // (token, K or V)
+    const bool in = item < 2 * p.T;
+    const int tok = item >> 1, which = item & 1;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (in)
+      raw = __ldg(reinterpret_cast<const uint4*>(
+                      p.qkv + (static_cast<size_t>(tok) * (p.nq + 2 * p.nkv) + p.nq +
+                               which * p.nkv + g) * kAttnHeadDim) +
+                  l);
+    const size_t row = static_cast<size_t>(g) * p.max_len + p.past + tok;
+    if constexpr (!k8) {
+      if (in)
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>((which ? p.cache[1] : p.cache[0])) + row * kAttnHeadDim)[l] =
+            raw;
+    } else {
+      float x[8];
+      unpack8(raw, x);
+      float amax = abs_max8(x);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      float scale;
+      const uint2 codes = kv8_codes(x, amax, scale);
+      if (in) {
+        reinterpret_cast<uint2*>(static_cast<uint8_t*>((which ? p.cache[1] : p.cache[0])) + row * kAttnHeadDim)[l] =
+            codes;
+        if (l == 0) (which ? p.cache_scale[1] : p.cache_scale[0])[row] = scale;
+      }
+    }
+  }
+}
+
+// 16 weights (already times 2^11 times the value scale over C) as three 16-byte
+// vectors of E5M2 terms: a = the leading 3 bits, b = the next of the rest, c =
+// the rest of that, rounded.  x - a and x - a - b are exact in fp16.
+__device__ __forceinline__ void split_weights(const float* w, uint4& a4, uint4& b4, uint4& c4) {
+  uint32_t a[4], b[4], c[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t av[2], bv[2], cv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __half2 x = __floats2half2_rn(w[4 * q + 2 * h], w[4 * q + 2 * h + 1]);
+      const uint32_t xb = *reinterpret_cast<const uint32_t*>(&x);
+      av[h] = xb & 0xFF00FF00u;
+      const __half2 r1 = __hsub2(x, *reinterpret_cast<const __half2*>(&av[h]));
+      const uint32_t r1b = *reinterpret_cast<const uint32_t*>(&r1);
+      bv[h] = r1b & 0xFF00FF00u;
+      const __half2 r2 = __hsub2(r1, *reinterpret_cast<const __half2*>(&bv[h]));
+      cv[h] = *reinterpret_cast<const uint32_t*>(&r2) + 0x00800080u;
+    }
+    a[q] = __byte_perm(av[0], av[1], 0x7531);
+    b[q] = __byte_perm(bv[0], bv[1], 0x7531);
+    c[q] = __byte_perm(cv[0], cv[1], 0x7531);
+  }
+  a4 = make_uint4(a[0], a[1], a[2], a[3]);
+  b4 = make_uint4(b[0], b[1], b[2], b[3]);
+  c4 = make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// TMEM columns [col, col + kCols) of this thread's lane.
+template <int kCols>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&v)[kCols]) {
+  if constexpr (kCols == 16) {
+    tmem_ld16(addr, v);
+  } else {
+#pragma unroll
+    for (int c = 0; c < kCols; c += 32)
+      tmem_ld32(addr + static_cast<uint32_t>(c), *reinterpret_cast<uint32_t(*)[32]>(v + c));
+  }
+}
+
+template <int kRows, bool k8>
+__global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRows, k8>::kBlocksPerSm)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                     const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
+  using Sh = TreeShape<kRows, k8>;
+  constexpr int kCols = Sh::kCols;
+  constexpr int kStages = Sh::kStages;
+  constexpr int kItems = Sh::kKItems;
+  constexpr int kSoftmax = 128 * Sh::kGroups;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = smem;
+  uint8_t* qs = ring + kStages * kTreeStageBytes;
+  uint8_t* ps = qs + Sh::kQBytes;                                   // [2 slots][parts]
+  float* m_s = reinterpret_cast<float*>(ps + 2 * Sh::kSlotBytes);   // running maxima
+  float* a_s = m_s + kRows;      // this raise's factor of O
+  float* al_s = a_s + kRows;     // this raise's factor of the sums
+  float* rf_s = al_s + kRows;    // 8 bits: score factor of each row
+  float* red = rf_s + kRows;     // [4][kRows]
+  int* red_c = reinterpret_cast<int*>(red + 4 * kRows);  // [2 warpgroups][4]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(red_c + 8);
+  uint64_t* full_bar = bars;                      // [kStages]
+  uint64_t* empty_bar = full_bar + kTreeMaxStages;
+  uint64_t* q_bar = empty_bar + kTreeMaxStages;   // the query operand is written
+  uint64_t* s_full = q_bar + 1;                   // [2] scores of a block in their slot
+  uint64_t* s_free = s_full + 2;                  // [2] slot read
+  uint64_t* p_full = s_free + 2;                  // [2] weights written, O rescaled
+  uint64_t* o_done = p_full + 2;                  // [2] the block's value product done
+  uint64_t* final_bar = o_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int chunk = blockIdx.x;
+  const int g = blockIdx.y;
+  const int grp = blockIdx.z;
+  const int blk0 = chunk * p.nb;
+  const int nbc = p.nblk - blk0 < p.nb ? p.nblk - blk0 : p.nb;  // at least 1
+  const int key0 = blk0 * 128;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    mbar_init(smem_u32(q_bar), kSoftmax / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_free[i]), kSoftmax / 32);
+      mbar_init(smem_u32(&p_full[i]), kSoftmax / 32);
+      mbar_init(smem_u32(&o_done[i]), 1);
+    }
+    mbar_init(smem_u32(final_bar), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), static_cast<uint32_t>(Sh::kTmemCols));
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t o_col = 2u * kRows;  // score slots at columns 0 and kRows, then O
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer
+      prefetch_tmap(&tmap_k);
+      prefetch_tmap(&tmap_v);
+      grid_dependency_wait();  // a preceding kernel may still write the cache
+      fence_proxy_async_global();
+      uint32_t issued = 0u, phases = 0u;
+      int s = 0;
+      uint32_t ph = 0u;
+      bool ok = true;
+      auto load = [&](bool is_v, int b) {
+        const int kb = key0 + b * 128;
+        for (int it = 0; it < kItems && ok; ++it) {
+          if (!wait_parity(smem_u32(&empty_bar[s]), ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(&full_bar[s]);
+          const uint32_t dst = smem_u32(ring + s * kTreeStageBytes);
+          mbar_arrive_expect_tx(fb, kTreeStageBytes);
+          if constexpr (k8) {
+            tma_load_3d(dst, is_v ? &tmap_v : &tmap_k, fb, 0, kb, g);
+          } else if (!is_v) {  // item: one 64-wide half of d, 128 keys
+            tma_load_3d(dst, &tmap_k, fb, it * 64, kb, g);
+          } else {             // item: 64 keys, both halves of d
+            tma_load_3d(dst, &tmap_v, fb, 0, kb + it * 64, g);
+            tma_load_3d(dst + kTreeStageBytes / 2, &tmap_v, fb, 64, kb + it * 64, g);
+          }
+          issued |= 1u << s;
+          phases = (phases & ~(1u << s)) | (ph << s);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      };
+      for (int b = 0; b <= nbc && ok; ++b) {
+        if (b < nbc) load(false, b);
+        if (b > 0) load(true, b - 1);
+      }
+      if (*abort_flag) {
+        for (int st = 0; st < kStages; ++st)
+          if (issued & (1u << st))
+            drain_wait(smem_u32(&full_bar[st]), (phases >> st) & 1u, 50ull * 1000ull * 1000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- MMA issuer, in the producer's order
+      bool ok = wait_parity(smem_u32(q_bar), 0, abort_flag);
+      tc_fence_after();
+      int s = 0;
+      uint32_t ph = 0u;
+      auto advance = [&] {
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      };
+      for (int b = 0; b <= nbc && ok; ++b) {
+        if (b < nbc) {
+          const int slot = b & 1;
+          if (b >= 2) ok = wait_parity(smem_u32(&s_free[slot]), ((b - 2) >> 1) & 1, abort_flag);
+          const uint32_t d = tmem + static_cast<uint32_t>(slot * kRows);
+          for (int it = 0; it < kItems && ok; ++it) {
+            ok = wait_parity(smem_u32(&full_bar[s]), ph, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
+            if constexpr (k8) {
+              constexpr uint32_t idesc = idesc_f8_f32(128, kRows, false, false, false);
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_f8(d, desc_kmajor_sw128(st + kk * 32u),
+                          desc_kmajor_sw128(smem_u32(qs) + part * (kRows * 128u) + kk * 32u), idesc,
+                          part + kk > 0 ? 1u : 0u);
+            } else {
+              constexpr uint32_t idesc = idesc_bf16_f32(128, kRows);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(d, desc_kmajor_sw128(st + kk * 32u),
+                          desc_kmajor_sw128(smem_u32(qs) + it * (kRows * 128u) + kk * 32u), idesc,
+                          it + kk > 0 ? 1u : 0u);
+            }
+            umma_commit(smem_u32(&empty_bar[s]));
+            advance();
+          }
+          if (!ok) break;
+          umma_commit(smem_u32(&s_full[slot]));
+        }
+        if (b > 0) {
+          const int v = b - 1, slot = v & 1;
+          ok = wait_parity(smem_u32(&p_full[slot]), (v >> 1) & 1, abort_flag);
+          const uint32_t pb = smem_u32(ps) + static_cast<uint32_t>(slot * Sh::kSlotBytes);
+          for (int it = 0; it < kItems && ok; ++it) {
+            ok = wait_parity(smem_u32(&full_bar[s]), ph, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
+            if constexpr (k8) {
+              // 32 keys a step: V 4096 bytes on, the weights 4 core matrices on
+              constexpr uint32_t idesc = idesc_f8_f32(128, kRows, true, true, true);
+#pragma unroll
+              for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_f8(tmem + o_col, desc_mnmajor_sw128(st + kk * 4096u, 0),
+                          desc_mnmajor_plain(pb + part * static_cast<uint32_t>(Sh::kPartBytes) +
+                                                 kk * 512u, 128, 2048),
+                          idesc, (v > 0 || part + kk > 0) ? 1u : 0u);
+            } else {
+              // 16 keys a step: V 2048 bytes on (its d halves 8 KB apart), the
+              // weights 2 core matrices on
+              constexpr uint32_t idesc = idesc_bf16_f32(128, kRows, true, true);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem + o_col,
+                          desc_mnmajor_sw128(st + kk * 2048u, kTreeStageBytes / 2),
+                          desc_mnmajor_plain(pb + (it * 4 + kk) * 256u, 128, 2048), idesc,
+                          (v > 0 || it + kk > 0) ? 1u : 0u);
+            }
+            umma_commit(smem_u32(&empty_bar[s]));
+            advance();
+          }
+          if (!ok) break;
+          umma_commit(smem_u32(&o_done[slot]));
+        }
+      }
+      umma_commit(smem_u32(final_bar));
+      drain_wait(smem_u32(final_bar), 0, 50ull * 1000ull * 1000ull);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax warps.  Thread r of a warpgroup owns TMEM lane r:
+    // key r of each block, and element r of O; warpgroup w owns query rows
+    // [w kCols, (w + 1) kCols).  Every thread takes the same barriers and
+    // arrivals whatever its waits returned.
+    grid_dependency_wait();  // qkv; and the partials may still be read
+    const int st = threadIdx.x - 64;
+    const int wg = st >> 7;
+    const int et = st & 127;
+    const int q4 = warp & 3;
+    const int r = q4 * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t bar_id = 1u + static_cast<uint32_t>(wg);
+    const int row0 = grp * kRows;
+    const int c0 = wg * kCols;
+    load_queries<kRows, k8>(p, g, row0, qs, rf_s, st, kSoftmax);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(q_bar));
+    append_rows<k8>(p, g, chunk + p.chunks * grp, p.chunks * p.groups, st, kSoftmax);
+    if (et < kCols) m_s[c0 + et] = kUnsetMax;
+    named_barrier_sync(3, kSoftmax);  // rf_s and m_s are written
+
+    float lsum[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) lsum[j] = 0.0f;
+    int c_exp = -100;  // 8 bits: C = 2^c_exp
+    bool ok = true;
+    for (int b = 0; b < nbc; ++b) {
+      const int slot = b & 1;
+      const int key = key0 + b * 128 + r;
+      const bool valid = key < p.past;
+      float kscale = p.scale_log2, vscale = 0.0f;
+      if constexpr (k8) {
+        const size_t at = static_cast<size_t>(g) * p.max_len + key;
+        kscale = valid ? __ldg(p.cache_scale[0] + at) : 0.0f;
+        vscale = valid ? __ldg(p.cache_scale[1] + at) : 0.0f;
+      }
+      ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&s_full[slot]), (b >> 1) & 1,
+                                                     abort_flag));
+      tc_fence_after();
+      uint32_t sv[kCols];
+      if (ok) {
+        tmem_ld_cols<kCols>(tmem + lane_addr + static_cast<uint32_t>(slot * kRows + c0), sv);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) sv[j] = 0u;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s_free[slot]));
+      // t: scores in base-2 units; the running maximum stays unless some t
+      // passes it by more than kLazyLog2
+      float t[kCols];
+      float over = kUnsetMax;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        float f = kscale;
+        if constexpr (k8) f *= rf_s[c0 + j];
+        t[j] = valid ? __uint_as_float(sv[j]) * f : neg_inf();
+        over = fmaxf(over, t[j] - m_s[c0 + j]);
+      }
+      bool raise = b == 0 || over > kLazyLog2;
+      if constexpr (k8) raise = raise || vscale > pow2i(c_exp);
+      raise = named_barrier_any(bar_id, 128, raise);
+      if (raise) {
+        // the block's maximum of every row (and of the value scales), over the
+        // lanes of a warp and then the four warps in order
+#pragma unroll
+        for (int c = 0; c < kCols; c += (kCols == 16 ? 16 : 32)) {
+          if constexpr (kCols == 16) {
+            float mx[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) mx[j] = t[j];
+            const float m = warp_rows_reduce<16, true>(mx, lane);
+            if ((lane & 1) == 0) red[q4 * kRows + c0 + ((lane >> 1) & 15)] = m;
+          } else {
+            float mx[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx[j] = t[c + j];
+            const float m = warp_rows_reduce<32, true>(mx, lane);
+            red[q4 * kRows + c0 + c + lane] = m;
+          }
+        }
+        int c_new = c_exp;
+        if constexpr (k8) {
+          const int e = __reduce_max_sync(0xffffffffu, scale_exponent(vscale));
+          if (lane == 0) red_c[wg * 4 + q4] = e;
+        }
+        named_barrier_sync(bar_id, 128);
+        if constexpr (k8) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) c_new = max(c_new, red_c[wg * 4 + w]);
+        }
+        if (et < kCols) {
+          const int n = c0 + et;
+          const float mo = m_s[n];
+          float mn = fmaxf(fmaxf(red[n], red[kRows + n]), fmaxf(red[2 * kRows + n], red[3 * kRows + n]));
+          mn = fmaxf(mo, mn);
+          const float al = exp2f(mo - mn);
+          m_s[n] = mn;
+          al_s[n] = al;
+          a_s[n] = k8 ? al * pow2i(c_exp - c_new < -126 ? -126 : c_exp - c_new) : al;
+        }
+        c_exp = c_new;
+        named_barrier_sync(bar_id, 128);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) lsum[j] *= al_s[c0 + j];
+        if (b > 0) {
+          // O holds the products of blocks 0 .. b - 1: wait for the last
+          ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[slot ^ 1]),
+                                                         ((b - 1) >> 1) & 1, abort_flag));
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+              uint32_t o[16];
+              const uint32_t at = tmem + lane_addr + o_col + static_cast<uint32_t>(c0 + c);
+              tmem_ld16(at, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * a_s[c0 + c + j]);
+              tmem_st16(at, o);
+            }
+            tmem_wait_st();
+          }
+        }
+      }
+      // the slot's weights are free once block b - 2's value product is done
+      if (b >= 2)
+        ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[slot]),
+                                                       ((b - 2) >> 1) & 1, abort_flag));
+      uint8_t* pslot = ps + slot * Sh::kSlotBytes;
+      float wf = 1.0f;
+      if constexpr (k8) wf = vscale * pow2i(kWeightShift - c_exp);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        float w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float e = exp2_fast(t[c + j] - m_s[c0 + c + j]);
+          lsum[c + j] += e;
+          w[j] = k8 ? e * wf : e;
+        }
+        if constexpr (k8) {
+          uint4 a4, b4, c4;
+          split_weights(w, a4, b4, c4);
+          uint8_t* at = pslot + ((c0 + c) / 16) * 2048 + r * 16;
+          *reinterpret_cast<uint4*>(at) = a4;
+          *reinterpret_cast<uint4*>(at + Sh::kPartBytes) = b4;
+          *reinterpret_cast<uint4*>(at + 2 * Sh::kPartBytes) = c4;
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4*>(pslot + ((c0 + c) / 8 + h) * 2048 + r * 16) =
+                make_uint4(pack_bf16x2(w[8 * h], w[8 * h + 1]),
+                           pack_bf16x2(w[8 * h + 2], w[8 * h + 3]),
+                           pack_bf16x2(w[8 * h + 4], w[8 * h + 5]),
+                           pack_bf16x2(w[8 * h + 6], w[8 * h + 7]));
+        }
+      }
+      fence_proxy_async_smem();  // the weights are read by the MMA through the async proxy
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&p_full[slot]));
+    }
+    // the rows' sums over the lanes, then the four warps in order
+#pragma unroll
+    for (int c = 0; c < kCols; c += (kCols == 16 ? 16 : 32)) {
+      if constexpr (kCols == 16) {
+        const float v = warp_rows_reduce<16, false>(lsum, lane);
+        if ((lane & 1) == 0) red[q4 * kRows + c0 + ((lane >> 1) & 15)] = v;
+      } else {
+        const float v =
+            warp_rows_reduce<32, false>(*reinterpret_cast<float(*)[32]>(lsum + c), lane);
+        red[q4 * kRows + c0 + c + lane] = v;
+      }
+    }
+    named_barrier_sync(bar_id, 128);
+    const size_t part = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks + chunk;
+    if (et < kCols && row0 + c0 + et < p.R) {
+      const int n = c0 + et;
+      float2 ml = make_float2(m_s[n], ((red[n] + red[kRows + n]) + red[2 * kRows + n]) +
+                                          red[3 * kRows + n]);
+      *reinterpret_cast<float2*>(p.part_ml + (part * kRows + n) * 2) = ml;
+    }
+    ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[(nbc - 1) & 1]),
+                                                   ((nbc - 1) >> 1) & 1, abort_flag));
+    tc_fence_after();
+    const float of = k8 ? pow2i(c_exp - kWeightShift) : 1.0f;
+    float* po = p.part_o + (part * kRows + c0) * kAttnHeadDim + r;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 16) {
+      uint32_t o[16];
+      if (ok) {
+        tmem_ld16(tmem + lane_addr + o_col + static_cast<uint32_t>(c0 + c), o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (row0 + c0 + c + j < p.R)
+          po[static_cast<size_t>(c + j) * kAttnHeadDim] = ok ? __uint_as_float(o[j]) * of : 0.0f;
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  grid_launch_dependents();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, static_cast<uint32_t>(Sh::kTmemCols));
+  }
+}
+
+struct TreeMergeParams {
+  int T, past, nq, nkv, G, rows, chunks, max_len;
+  int words;        // mask words per token
+  int warps;        // warps per (token, query head): 1, 2, 4 or 8
+  float scale;      // 1 / sqrt(d)
+  const uint16_t* qkv;
+  const void* cache[2];
+  const float* cache_scale[2];
+  const unsigned long long* mask;  // [T][words], or null: j <= i
+  const float* part_o;
+  const float* part_ml;
+  uint16_t* ctx;    // [T, nq d]
+};
+
+constexpr int kMergeWarps = 8;
+constexpr int kMergeChunks = 8;  // partials a warp has in flight
+constexpr int kMergeTokens = 4;  // new tokens a warp has in flight
+
+// One running (maximum, sum, weighted sum) of a warp, lane l owning elements
+// 4 l .. 4 l + 3; maxima in base-2 units.
+struct MergeState {
+  float m, l;
+  float4 o;
+};
+
+__device__ __forceinline__ void merge_in(MergeState& a, float m, float l, const float4& o,
+                                         float weight) {
+  if (m > a.m) {
+    const float s = a.m == neg_inf() ? 0.0f : exp2f(a.m - m);
+    a.o.x *= s;
+    a.o.y *= s;
+    a.o.z *= s;
+    a.o.w *= s;
+    a.l *= s;
+    a.m = m;
+  }
+  const float w = m == neg_inf() ? 0.0f : exp2f(m - a.m);
+  if (m == neg_inf()) return;
+  a.o.x = fmaf(w * weight, o.x, a.o.x);
+  a.o.y = fmaf(w * weight, o.y, a.o.y);
+  a.o.z = fmaf(w * weight, o.z, a.o.z);
+  a.o.w = fmaf(w * weight, o.w, a.o.w);
+  a.l = fmaf(w, l, a.l);
+}
+
+// Four elements of a cached row.
+template <bool k8>
+__device__ __forceinline__ uint2 cache_raw(const void* cache, size_t row, int lane) {
+  if constexpr (k8)
+    return make_uint2(__ldcg(reinterpret_cast<const unsigned int*>(
+                                 static_cast<const uint8_t*>(cache) + row * kAttnHeadDim) + lane),
+                      0u);
+  else
+    return __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(cache) +
+                                                 row * kAttnHeadDim) + lane);
+}
+
+template <bool k8>
+__device__ __forceinline__ float4 cache_values(const uint2& raw) {
+  if constexpr (k8) {
+    const __half2 a(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(raw.x), __NV_E4M3));
+    const __half2 b(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(raw.x >> 16), __NV_E4M3));
+    const float2 fa = __half22float2(a), fb = __half22float2(b);
+    return make_float4(fa.x, fa.y, fb.x, fb.y);
+  } else {
+    return make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
+                       __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u));
+  }
+}
+
+// p.warps warps per (token, query head).  Warp w takes chunks w, w + warps, ...
+// and the visible new tokens j = w, w + warps, ... in order; the warps' states
+// are then added in order.  Bit-identical from run to run.
+template <bool k8>
+__global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const TreeMergeParams p) {
+  __shared__ float4 red_o[kMergeWarps][32];
+  __shared__ float red_l[kMergeWarps], red_m[kMergeWarps];
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = warp % p.warps;
+  const int wid = blockIdx.x * (kMergeWarps / p.warps) + warp / p.warps;
+  MergeState st{neg_inf(), 0.0f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const bool in = wid < p.T * p.nq;
+  const int i = in ? wid / p.nq : 0;
+  const int h = in ? wid % p.nq : 0;
+  const int g = h / p.G;
+  if (in) {
+    const int rr = i * p.G + h % p.G;
+    const int grp = rr / p.rows, n = rr % p.rows;
+    const size_t base = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks;
+    for (int c0 = w; c0 < p.chunks; c0 += p.warps * kMergeChunks) {
+      float2 ml[kMergeChunks];
+      float4 o[kMergeChunks];
+#pragma unroll
+      for (int k = 0; k < kMergeChunks; ++k) {
+        const int c = c0 + k * p.warps;
+        if (c < p.chunks) {
+          const size_t at = (base + c) * p.rows + n;
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
+          o[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kAttnHeadDim) + lane);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeChunks; ++k)
+        if (c0 + k * p.warps < p.chunks) merge_in(st, ml[k].x, ml[k].y, o[k], 1.0f);
+    }
+    // the new tokens that row i sees
+    const float f = p.scale * 1.4426950408889634f;
+    const float4 q = cache_values<false>(
+        __ldg(reinterpret_cast<const uint2*>(
+                  p.qkv + (static_cast<size_t>(i) * (p.nq + 2 * p.nkv) + h) * kAttnHeadDim) +
+              lane));
+    const unsigned long long mine =
+        (p.warps == 8 ? 0x0101010101010101ull : p.warps == 4 ? 0x1111111111111111ull
+         : p.warps == 2 ? 0x5555555555555555ull : ~0ull) << w;
+    const int words = (p.T + 63) / 64;
+    const size_t row0 = static_cast<size_t>(g) * p.max_len + p.past;
+    for (int word = 0; word < words; ++word) {
+      const int left = p.T - word * 64;                       // tokens from this word on
+      unsigned long long bits = left >= 64 ? ~0ull : (1ull << left) - 1ull;
+      if (p.mask != nullptr) {
+        bits &= __ldg(p.mask + static_cast<size_t>(i) * p.words + word);
+      } else {
+        const int upto = i - word * 64 + 1;                   // tokens j <= i
+        bits &= upto >= 64 ? ~0ull : upto > 0 ? (1ull << upto) - 1ull : 0ull;
+      }
+      bits &= mine;
+      while (bits != 0ull) {
+        uint2 kr[kMergeTokens], vr[kMergeTokens];
+        float ks[kMergeTokens], vs[kMergeTokens], s[kMergeTokens];
+        int count = 0;
+#pragma unroll
+        for (int k = 0; k < kMergeTokens; ++k) {
+          if (bits != 0ull) {
+            const int j = word * 64 + __ffsll(static_cast<long long>(bits)) - 1;
+            bits &= bits - 1ull;
+            kr[k] = cache_raw<k8>(p.cache[0], row0 + j, lane);
+            vr[k] = cache_raw<k8>(p.cache[1], row0 + j, lane);
+            ks[k] = k8 ? __ldcg(p.cache_scale[0] + row0 + j) : 1.0f;
+            vs[k] = k8 ? __ldcg(p.cache_scale[1] + row0 + j) : 1.0f;
+            count = k + 1;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kMergeTokens; ++k) {
+          s[k] = 0.0f;
+          if (k < count) {
+            const float4 kv = cache_values<k8>(kr[k]);
+            s[k] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, q.w * kv.w)));
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int k = 0; k < kMergeTokens; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+#pragma unroll
+        for (int k = 0; k < kMergeTokens; ++k)
+          if (k < count) merge_in(st, s[k] * ks[k] * f, 1.0f, cache_values<k8>(vr[k]), vs[k]);
+      }
+    }
+  }
+  if (p.warps > 1) {
+    red_o[warp][lane] = st.o;
+    if (lane == 0) {
+      red_l[warp] = st.l;
+      red_m[warp] = st.m;
+    }
+    __syncthreads();
+    if (w != 0) return;
+    float m = st.m;
+    for (int k = 1; k < p.warps; ++k) m = fmaxf(m, red_m[warp + k]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.0f;
+    for (int k = 0; k < p.warps; ++k) {
+      const float mk = red_m[warp + k];
+      const float f = mk == neg_inf() ? 0.0f : exp2f(mk - m);
+      const float4 v = red_o[warp + k][lane];
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z);
+      o.w = fmaf(f, v.w, o.w);
+      l = fmaf(f, red_l[warp + k], l);
+    }
+    st.o = o;
+    st.l = l;
+  }
+  if (!in) return;
+  const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;  // a row that sees nothing is zero
+  uint2 packed;
+  packed.x = pack_bf16x2(st.o.x * inv, st.o.y * inv);
+  packed.y = pack_bf16x2(st.o.z * inv, st.o.w * inv);
+  *(reinterpret_cast<uint2*>(p.ctx + static_cast<size_t>(i) * p.nq * kAttnHeadDim +
+                             static_cast<size_t>(h) * kAttnHeadDim) + lane) = packed;
+}
+
+}  // namespace tpb

@@ -8,17 +8,21 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cstdint>
 #include <cstdio>
 #include <mutex>
 
 #include "attn_kernel.cuh"
 #include "attn_prefill_kernel.cuh"
+#include "attn_tree_kernel.cuh"
 #include "colsum_kernel.cuh"
 #include "diag_kernel.cuh"
+#include "kv_cache_kernel.cuh"
 #include "norm_kernel.cuh"
 #include "pair_kernel.cuh"
 #include "ptx.cuh"
+#include "qk_norm_kernel.cuh"
 #include "stream_kernel.cuh"
 #include "tiled_kernel.cuh"
 
@@ -105,6 +109,26 @@ PairKernel pair_kernel_for(int epi, bool a_mn, bool b_mn) {
   return nullptr;
 }
 
+// The tree-attention kernel's instantiations by query rows per block (16, 32,
+// 64, 128), for a bf16 and for an 8-bit cache.
+using TreeKernel = void (*)(const CUtensorMap, const CUtensorMap, const tpb::TreeParams);
+struct TreeLaunch {
+  TreeKernel kernel;
+  int rows, threads, smem, blocks_per_sm;
+};
+template <int kRows, bool k8>
+constexpr TreeLaunch tree_launch() {
+  using Sh = tpb::TreeShape<kRows, k8>;
+  return TreeLaunch{tpb::attn_tree_kernel<kRows, k8>, kRows, Sh::kThreads, Sh::kSmem,
+                    Sh::kBlocksPerSm};
+}
+const TreeLaunch kTreeLaunches[2][4] = {
+    {tree_launch<16, false>(), tree_launch<32, false>(), tree_launch<64, false>(),
+     tree_launch<128, false>()},
+    {tree_launch<16, true>(), tree_launch<32, true>(), tree_launch<64, true>(),
+     tree_launch<128, true>()},
+};
+
 const DeviceInfo* device_info() {
   int dev = 0;
   if (!cuda_ok(cudaGetDevice(&dev), "cudaGetDevice") || dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -158,6 +182,15 @@ const DeviceInfo* device_info() {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                "cudaFuncSetAttribute"))
     return nullptr;
+  for (const auto& kind : kTreeLaunches)
+    for (const TreeLaunch& l : kind)
+      if (!cuda_ok(cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        l.smem),
+                   "cudaFuncSetAttribute") ||
+          !cuda_ok(cudaFuncSetAttribute(l.kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                        cudaSharedmemCarveoutMaxShared),
+                   "cudaFuncSetAttribute"))
+        return nullptr;
   d.sms = sms;
   d.max_smem = smem;
   d.ready = true;
@@ -657,6 +690,279 @@ bool make_tmap_rows3(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
   return ok;
 }
 
+// The same view of 8-bit rows of d = 128 codes: a box {128, 128 rows, 1} lands
+// as 128 rows of 128 bytes with 128-byte swizzling.
+bool make_tmap_rows3_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t outer,
+                        uint64_t outer_stride) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return cuda_ok(cudaErrorSymbolNotFound, "cuTensorMapEncodeTiled lookup");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(tpb::kAttnHeadDim), rows, outer};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(tpb::kAttnHeadDim), outer_stride};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(tpb::kAttnHeadDim), 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const bool ok = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  if (!ok) cuda_ok(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (8-bit rows3)");
+  return ok;
+}
+
+// ------------------------------------------------------------------ heads' rows (norms, caches)
+
+bool heads_ok(int T, int past, int nq, int nkv) {
+  return T >= 1 && past >= 0 && nq >= 1 && nkv >= 1 && nq % nkv == 0;
+}
+
+bool row_dim_ok(int d) { return d >= 16 && d <= tpb::kQkMaxDim && d % 16 == 0; }
+
+// Lanes that hold one row of d bf16 elements, 8 each.
+int row_lanes(int d) { return next_pow2(d / 8); }
+
+// An element index of a cache or of qkv stays far inside 64 bits.
+bool cache_ok(int nkv, int max_len, int d) {
+  return max_len >= 1 && max_len <= INT_MAX - 256 &&
+         static_cast<long long>(nkv) * max_len * d <= (1ll << 40) && nkv <= 32767;
+}
+
+tp_status check_qk(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf16* gamma_k,
+                   const float* inv_freq, const int* positions, int T, int past, int nq, int nkv,
+                   int d, int rot, int layout, float eps, int t) {
+  if (qkv == nullptr || (gamma_q == nullptr) != (gamma_k == nullptr) ||
+      (rot > 0 && inv_freq == nullptr))
+    return TP_ERR_NULL;
+  if (!aligned16(qkv) || !aligned16(gamma_q) || !aligned16(gamma_k) || !aligned16(inv_freq) ||
+      !aligned16(positions))
+    return TP_ERR_ALIGN;
+  if (!heads_ok(T, past, nq, nkv) || !row_dim_ok(d) || rot < 0 || rot > d || rot % 16 != 0 ||
+      !(eps >= 0.0f) || static_cast<long long>(past) + T > INT_MAX ||
+      static_cast<long long>(nq) + 2ll * nkv > (1 << 20))
+    return TP_ERR_SHAPE;
+  if (layout != TP_ROPE_HALF && layout != TP_ROPE_PAIRS) return TP_ERR_UNSUPPORTED;
+  if (t < 1 || nq % t != 0 || nkv % t != 0) return TP_ERR_TP_DEGREE;
+  return TP_OK;
+}
+
+tpb::QkParams qk_params(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf16* gamma_k,
+                        const float* inv_freq, const int* positions, int T, int past, int nq,
+                        int nkv, int d, int rot, int layout, float eps, tp_bf16* out,
+                        bool in_place) {
+  tpb::QkParams p{};
+  p.x = qkv;
+  p.gamma_q = gamma_q;
+  p.gamma_k = gamma_k;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.out = out;
+  p.T = T;
+  p.past = past;
+  p.nq = nq;
+  p.nkv = nkv;
+  p.d = d;
+  p.rot = rot;
+  p.lanes = row_lanes(d);
+  p.heads = nq + (in_place ? 1 : 2) * nkv;
+  p.pairs = layout == TP_ROPE_PAIRS ? 1 : 0;
+  p.eps = eps;
+  return p;
+}
+
+// Blocks of the gradient kernel: a function of T only, so the gains' sums are
+// taken in the same order on every device.
+int qk_backward_blocks(int T) { return T < tpb::kQkMaxBlocks ? T : tpb::kQkMaxBlocks; }
+
+cudaLaunchConfig_t launch_config(dim3 grid, int threads, int smem, cudaStream_t stream,
+                                 cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = static_cast<unsigned>(launch_attrs(attr, 0));
+  return cfg;
+}
+
+tp_status check_append(const tp_bf16* qkv, const int* rows, const void* k, const void* v, int T,
+                       int n, int past, int max_len, int nq, int nkv, int d, int t) {
+  if (qkv == nullptr || k == nullptr || v == nullptr) return TP_ERR_NULL;
+  if (!aligned16(qkv) || !aligned16(rows) || !aligned16(k) || !aligned16(v)) return TP_ERR_ALIGN;
+  if (!heads_ok(T, past, nq, nkv) || !row_dim_ok(d) || n < 1 || (rows == nullptr && n > T) ||
+      !cache_ok(nkv, max_len, d) || static_cast<long long>(past) + n > max_len)
+    return TP_ERR_SHAPE;
+  if (t < 1 || nq % t != 0 || nkv % t != 0) return TP_ERR_TP_DEGREE;
+  return TP_OK;
+}
+
+template <bool k8>
+tp_status launch_append(const tpb::KvAppendParams& p, cudaStream_t stream) {
+  const int per_block = tpb::kCacheThreads / p.lanes;
+  const int blocks = (p.n + per_block - 1) / per_block;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = launch_config(
+      dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(2 * p.nkv), 1), tpb::kCacheThreads,
+      0, stream, attr);
+  return cuda_ok(cudaLaunchKernelEx(&cfg, tpb::kv_append_rows_kernel<k8>, p),
+                 "launch kv_append_rows_kernel")
+             ? TP_OK
+             : TP_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ attention of a few new tokens
+
+constexpr int kTreeSms = 148;  // the plan is a function of the sizes only, as plan_attn's
+
+// Query rows per block: the smallest of 16, 32, 64 and 128 that holds the T G
+// rows of a head, so that the cache is read once; row groups of 128 above
+// that.  Chunks per head: the fewest key blocks on the busiest SM, counting
+// three for a block's set-up and partial.
+tp_status plan_tree(int T, int past, int nq, int nkv, tpb::TreeParams& p, int& which,
+                    size_t& part_o_bytes, size_t& part_ml_bytes) {
+  p = tpb::TreeParams{};
+  p.T = T;
+  p.past = past;
+  p.nq = nq;
+  p.nkv = nkv;
+  p.G = nq / nkv;
+  if (T > tpb::kTreeMaxTokens || p.G > 16) return TP_ERR_UNSUPPORTED;
+  p.R = T * p.G;
+  which = p.R <= 16 ? 0 : p.R <= 32 ? 1 : p.R <= 64 ? 2 : 3;
+  const TreeLaunch& l = kTreeLaunches[0][which];
+  p.groups = (p.R + l.rows - 1) / l.rows;
+  p.nblk = past / 128 + (past % 128 != 0 ? 1 : 0);
+  p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(tpb::kAttnHeadDim));
+  if (p.nblk > 0) {
+    const long long slots = static_cast<long long>(kTreeSms) * l.blocks_per_sm;
+    const long long per_chunk = static_cast<long long>(nkv) * p.groups;
+    long long best = 0;
+    const int most = p.nblk < 296 ? p.nblk : 296;
+    for (int c = 1; c <= most; ++c) {
+      const int nb = (p.nblk + c - 1) / c;
+      const int chunks = (p.nblk + nb - 1) / nb;
+      const long long waves = (per_chunk * chunks + slots - 1) / slots;
+      const long long cost = waves * (nb + 3);
+      if (best == 0 || cost < best) {
+        best = cost;
+        p.nb = nb;
+        p.chunks = chunks;
+      }
+    }
+  }
+  const size_t rows = static_cast<size_t>(p.groups) * nkv * p.chunks * l.rows;
+  part_o_bytes = rows * tpb::kAttnHeadDim * 4;
+  part_ml_bytes = (rows * 2 * 4 + 255) / 256 * 256;
+  return TP_OK;
+}
+
+template <bool k8>
+tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_cache, float* v_scale,
+                   const uint64_t* mask, int T, int past, int max_len, int nq, int nkv, int d,
+                   int t, tp_bf16* ctx, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream) {
+  if (qkv == nullptr || k_cache == nullptr || v_cache == nullptr || ctx == nullptr ||
+      (k8 && (k_scale == nullptr || v_scale == nullptr)))
+    return TP_ERR_NULL;
+  if (!aligned16(qkv) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(ctx) ||
+      !aligned16(k_scale) || !aligned16(v_scale) || !aligned16(mask))
+    return TP_ERR_ALIGN;
+  if (!heads_ok(T, past, nq, nkv) || d < 1 || !cache_ok(nkv, max_len, d) ||
+      static_cast<long long>(past) + T > max_len)
+    return TP_ERR_SHAPE;
+  if (d != tpb::kAttnHeadDim) return TP_ERR_UNSUPPORTED;
+  if (t < 1 || nq % t != 0 || nkv % t != 0) return TP_ERR_TP_DEGREE;
+  tpb::TreeParams p;
+  int which = 0;
+  size_t po = 0, pml = 0;
+  const tp_status planned = plan_tree(T, past, nq, nkv, p, which, po, pml);
+  if (planned != TP_OK) return planned;
+  if (po + pml > 0) {
+    if (workspace == nullptr || workspace_bytes < po + pml) return TP_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TP_ERR_ALIGN;
+  }
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return TP_ERR_CUDA;
+  const TreeLaunch& l = kTreeLaunches[k8 ? 1 : 0][which];
+  if (l.smem > dev->max_smem) return TP_ERR_UNSUPPORTED;
+  p.max_len = max_len;
+  p.qkv = qkv;
+  p.cache[0] = k_cache;
+  p.cache[1] = v_cache;
+  p.cache_scale[0] = k_scale;
+  p.cache_scale[1] = v_scale;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + po);
+  cudaLaunchAttribute attr[1];
+  if (past > 0) {
+    // 1. the cached keys, chunk by chunk, and the new keys and values behind them
+    CUtensorMap tk, tv;
+    const uint64_t outer = static_cast<uint64_t>(max_len) * d;
+    const bool maps =
+        k8 ? make_tmap_rows3_u8(&tk, k_cache, static_cast<uint64_t>(past),
+                                static_cast<uint64_t>(nkv), outer) &&
+                 make_tmap_rows3_u8(&tv, v_cache, static_cast<uint64_t>(past),
+                                    static_cast<uint64_t>(nkv), outer)
+           : make_tmap_rows3(&tk, k_cache, static_cast<uint64_t>(past), static_cast<uint64_t>(nkv),
+                             static_cast<uint64_t>(d), outer, 128, 1) &&
+                 make_tmap_rows3(&tv, v_cache, static_cast<uint64_t>(past),
+                                 static_cast<uint64_t>(nkv), static_cast<uint64_t>(d), outer, 64, 1);
+    if (!maps) return TP_ERR_CUDA;
+    cudaLaunchConfig_t cfg =
+        launch_config(dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(nkv),
+                           static_cast<unsigned>(p.groups)),
+                      l.threads, l.smem, stream, attr);
+    if (!cuda_ok(cudaLaunchKernelEx(&cfg, l.kernel, tk, tv, p), "launch attn_tree_kernel"))
+      return TP_ERR_CUDA;
+  } else {
+    tpb::KvAppendParams a{};
+    a.qkv = qkv;
+    a.cache[0] = k_cache;
+    a.cache[1] = v_cache;
+    a.scale[0] = k_scale;
+    a.scale[1] = v_scale;
+    a.T = a.n = T;
+    a.past = past;
+    a.max_len = max_len;
+    a.nq = nq;
+    a.nkv = nkv;
+    a.d = d;
+    a.lanes = row_lanes(d);
+    const tp_status s = launch_append<k8>(a, stream);
+    if (s != TP_OK) return s;
+  }
+  // 2. the partials and the new tokens that each row sees
+  tpb::TreeMergeParams m{};
+  m.T = T;
+  m.past = past;
+  m.nq = nq;
+  m.nkv = nkv;
+  m.G = p.G;
+  m.rows = l.rows;
+  m.chunks = p.chunks;
+  m.max_len = max_len;
+  m.words = (T + 63) / 64;
+  m.scale = 1.0f / sqrtf(static_cast<float>(d));
+  m.qkv = qkv;
+  m.cache[0] = k_cache;
+  m.cache[1] = v_cache;
+  m.cache_scale[0] = k_scale;
+  m.cache_scale[1] = v_scale;
+  m.mask = reinterpret_cast<const unsigned long long*>(mask);
+  m.part_o = p.part_o;
+  m.part_ml = p.part_ml;
+  m.ctx = ctx;
+  // about four partials or tokens per warp
+  const int items = p.chunks + (mask != nullptr ? (T < 8 ? T : 8) : (T + 1) / 2);
+  m.warps = items <= 4 ? 1 : items <= 8 ? 2 : items <= 16 ? 4 : 8;
+  const int per_block = tpb::kMergeWarps / m.warps;
+  cudaLaunchConfig_t cfg =
+      launch_config(dim3(static_cast<unsigned>((T * nq + per_block - 1) / per_block), 1, 1),
+                    tpb::kMergeWarps * 32, 0, stream, attr);
+  return cuda_ok(cudaLaunchKernelEx(&cfg, tpb::attn_tree_merge_kernel<k8>, m),
+                 "launch attn_tree_merge_kernel")
+             ? TP_OK
+             : TP_ERR_CUDA;
+}
+
 // ------------------------------------------------------------------ checks
 
 tp_status check_linear(const void* x, const void* w, const void* b, const void* out, int T, int K,
@@ -1009,6 +1315,215 @@ tp_status tp_sp_add_rmsnorm(const tp_bf16* y, const tp_bf16* residual, const tp_
               : cudaLaunchKernelEx(&cfg, tpb::add_rmsnorm_kernel<false>, y, residual, gamma, H, eps,
                                    r_out, n_out);
   return cuda_ok(e, "launch add_rmsnorm_kernel") ? TP_OK : TP_ERR_CUDA;
+}
+
+tp_status tp_qk_norm_rope(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf16* gamma_k,
+                          const float* inv_freq, const int32_t* positions, int T, int past,
+                          int n_q_heads, int n_kv_heads, int head_dim, int rot_dim, int layout,
+                          float eps, int tp_degree, tp_bf16* out, tp_stream_t stream) {
+  if (out == nullptr) return TP_ERR_NULL;
+  if (!aligned16(out)) return TP_ERR_ALIGN;
+  const tp_status s = check_qk(qkv, gamma_q, gamma_k, inv_freq, positions, T, past, n_q_heads,
+                               n_kv_heads, head_dim, rot_dim, layout, eps, tp_degree);
+  if (s != TP_OK) return s;
+  tpb::QkParams p = qk_params(qkv, gamma_q, gamma_k, inv_freq, positions, T, past, n_q_heads,
+                              n_kv_heads, head_dim, rot_dim, layout, eps, out, out == qkv);
+  // one block holds 8 x 32 / lanes heads at a time; few tokens share their
+  // heads among blocks until about two blocks per SM have work
+  const int step = tpb::kQkThreads / p.lanes;
+  const int most = (p.heads + step - 1) / step;
+  p.slices = T >= 296 ? 1 : (296 + T - 1) / T;
+  p.slices = p.slices > most ? most : p.slices;
+  if (static_cast<long long>(T) * p.slices > INT_MAX) return TP_ERR_SHAPE;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = launch_config(dim3(static_cast<unsigned>(T * p.slices), 1, 1),
+                                         tpb::kQkThreads, 0,
+                                         reinterpret_cast<cudaStream_t>(stream), attr);
+  return cuda_ok(cudaLaunchKernelEx(&cfg, tpb::qk_norm_rope_kernel, p), "launch qk_norm_rope_kernel")
+             ? TP_OK
+             : TP_ERR_CUDA;
+}
+
+size_t tp_qk_norm_rope_backward_workspace_bytes(int T, int head_dim) {
+  if (T < 1 || !row_dim_ok(head_dim)) return 0;
+  return (static_cast<size_t>(qk_backward_blocks(T)) * 2u * static_cast<size_t>(head_dim) * 4u +
+          255u) / 256u * 256u;
+}
+
+tp_status tp_qk_norm_rope_backward(const tp_bf16* qkv, const tp_bf16* gamma_q,
+                                   const tp_bf16* gamma_k, const float* inv_freq,
+                                   const int32_t* positions, const tp_bf16* dout, int T, int past,
+                                   int n_q_heads, int n_kv_heads, int head_dim, int rot_dim,
+                                   int layout, float eps, int tp_degree, tp_bf16* dqkv,
+                                   tp_bf16* dgamma_q, tp_bf16* dgamma_k, void* workspace,
+                                   size_t workspace_bytes, tp_stream_t stream) {
+  const bool norm = gamma_q != nullptr;
+  if (dout == nullptr || dqkv == nullptr ||
+      (norm && (dgamma_q == nullptr || dgamma_k == nullptr)))
+    return TP_ERR_NULL;
+  if (!aligned16(dout) || !aligned16(dqkv) || !aligned16(dgamma_q) || !aligned16(dgamma_k))
+    return TP_ERR_ALIGN;
+  tp_status s = check_qk(qkv, gamma_q, gamma_k, inv_freq, positions, T, past, n_q_heads,
+                         n_kv_heads, head_dim, rot_dim, layout, eps, tp_degree);
+  if (s != TP_OK) return s;
+  if (norm) {
+    if (workspace == nullptr ||
+        workspace_bytes < tp_qk_norm_rope_backward_workspace_bytes(T, head_dim))
+      return TP_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TP_ERR_ALIGN;
+  }
+  tpb::QkParams p = qk_params(qkv, gamma_q, gamma_k, inv_freq, positions, T, past, n_q_heads,
+                              n_kv_heads, head_dim, rot_dim, layout, eps, dqkv, dqkv == dout);
+  p.dy = dout;
+  p.partial = static_cast<float*>(workspace);
+  const int blocks = qk_backward_blocks(T);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg =
+      launch_config(dim3(static_cast<unsigned>(blocks), 1, 1), tpb::kQkThreads, 0, st, attr);
+  if (!cuda_ok(cudaLaunchKernelEx(&cfg, tpb::qk_norm_rope_backward_kernel, p),
+               "launch qk_norm_rope_backward_kernel"))
+    return TP_ERR_CUDA;
+  if (!norm) return TP_OK;
+  cfg = launch_config(dim3(static_cast<unsigned>(2 * head_dim / 16), 1, 1),
+                      16 * tpb::kQkReduceLanes, 0, st, attr);
+  return cuda_ok(cudaLaunchKernelEx(&cfg, tpb::qk_gain_reduce_kernel,
+                                    static_cast<const float*>(p.partial), blocks, head_dim,
+                                    dgamma_q, dgamma_k),
+                 "launch qk_gain_reduce_kernel")
+             ? TP_OK
+             : TP_ERR_CUDA;
+}
+
+tp_status tp_kv_append(const tp_bf16* qkv, const int32_t* rows, tp_bf16* k_cache, tp_bf16* v_cache,
+                       int T, int n, int past, int max_len, int n_q_heads, int n_kv_heads,
+                       int head_dim, int tp_degree, tp_stream_t stream) {
+  const tp_status s = check_append(qkv, rows, k_cache, v_cache, T, n, past, max_len, n_q_heads,
+                                   n_kv_heads, head_dim, tp_degree);
+  if (s != TP_OK) return s;
+  tpb::KvAppendParams p{};
+  p.qkv = qkv;
+  p.rows = rows;
+  p.cache[0] = k_cache;
+  p.cache[1] = v_cache;
+  p.T = T;
+  p.n = n;
+  p.past = past;
+  p.max_len = max_len;
+  p.nq = n_q_heads;
+  p.nkv = n_kv_heads;
+  p.d = head_dim;
+  p.lanes = row_lanes(head_dim);
+  return launch_append<false>(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tp_status tp_kv8_append(const tp_bf16* qkv, const int32_t* rows, uint8_t* k_cache, float* k_scale,
+                        uint8_t* v_cache, float* v_scale, int T, int n, int past, int max_len,
+                        int n_q_heads, int n_kv_heads, int head_dim, int tp_degree,
+                        tp_stream_t stream) {
+  if (k_scale == nullptr || v_scale == nullptr) return TP_ERR_NULL;
+  if (!aligned16(k_scale) || !aligned16(v_scale)) return TP_ERR_ALIGN;
+  const tp_status s = check_append(qkv, rows, k_cache, v_cache, T, n, past, max_len, n_q_heads,
+                                   n_kv_heads, head_dim, tp_degree);
+  if (s != TP_OK) return s;
+  tpb::KvAppendParams p{};
+  p.qkv = qkv;
+  p.rows = rows;
+  p.cache[0] = k_cache;
+  p.cache[1] = v_cache;
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.T = T;
+  p.n = n;
+  p.past = past;
+  p.max_len = max_len;
+  p.nq = n_q_heads;
+  p.nkv = n_kv_heads;
+  p.d = head_dim;
+  p.lanes = row_lanes(head_dim);
+  return launch_append<true>(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tp_status tp_kv8_read(const uint8_t* k_cache, const float* k_scale, const uint8_t* v_cache,
+                      const float* v_scale, int start, int count, int max_len, int n_kv_heads,
+                      int head_dim, int tp_degree, tp_bf16* k_out, tp_bf16* v_out, int out_len,
+                      tp_stream_t stream) {
+  if (k_cache == nullptr || k_scale == nullptr || v_cache == nullptr || v_scale == nullptr ||
+      k_out == nullptr || v_out == nullptr)
+    return TP_ERR_NULL;
+  if (!aligned16(k_cache) || !aligned16(k_scale) || !aligned16(v_cache) || !aligned16(v_scale) ||
+      !aligned16(k_out) || !aligned16(v_out))
+    return TP_ERR_ALIGN;
+  if (start < 0 || count < 1 || n_kv_heads < 1 || !row_dim_ok(head_dim) ||
+      !cache_ok(n_kv_heads, max_len, head_dim) || !cache_ok(n_kv_heads, out_len, head_dim) ||
+      static_cast<long long>(start) + count > max_len ||
+      static_cast<long long>(start) + count > out_len)
+    return TP_ERR_SHAPE;
+  if (tp_degree < 1 || n_kv_heads % tp_degree != 0) return TP_ERR_TP_DEGREE;
+  tpb::Kv8ReadParams p{};
+  p.codes[0] = k_cache;
+  p.codes[1] = v_cache;
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.out[0] = k_out;
+  p.out[1] = v_out;
+  p.start = start;
+  p.count = count;
+  p.max_len = max_len;
+  p.out_len = out_len;
+  p.d = head_dim;
+  const long long pieces = static_cast<long long>(count) * (head_dim / 16);
+  const long long per_block = static_cast<long long>(tpb::kCacheThreads) * tpb::kReadBatch;
+  const long long blocks = (pieces + per_block - 1) / per_block;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = launch_config(
+      dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(2 * n_kv_heads), 1),
+      tpb::kCacheThreads, 0, reinterpret_cast<cudaStream_t>(stream), attr);
+  return cuda_ok(cudaLaunchKernelEx(&cfg, tpb::kv8_read_kernel, p), "launch kv8_read_kernel")
+             ? TP_OK
+             : TP_ERR_CUDA;
+}
+
+tp_status tp_tree_mask(const int32_t* parents, int T, uint64_t* mask) {
+  if (parents == nullptr || mask == nullptr) return TP_ERR_NULL;
+  if (T < 1 || T > tpb::kTreeMaxTokens) return TP_ERR_SHAPE;
+  const int words = (T + 63) / 64;
+  for (int i = 0; i < T; ++i)
+    if (parents[i] < -1 || parents[i] >= i) return TP_ERR_SHAPE;
+  for (int i = 0; i < T; ++i) {
+    for (int w = 0; w < words; ++w)
+      mask[i * words + w] = parents[i] < 0 ? 0ull : mask[parents[i] * words + w];
+    mask[i * words + i / 64] |= 1ull << (i % 64);
+  }
+  return TP_OK;
+}
+
+size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads, int head_dim) {
+  if (!heads_ok(T, past, n_q_heads, n_kv_heads) || head_dim != tpb::kAttnHeadDim) return 0;
+  tpb::TreeParams p;
+  int which = 0;
+  size_t po = 0, pml = 0;
+  if (plan_tree(T, past, n_q_heads, n_kv_heads, p, which, po, pml) != TP_OK) return 0;
+  return po + pml;
+}
+
+tp_status tp_attn_tree(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,
+                       const uint64_t* tree_mask, int T, int past, int max_len, int n_q_heads,
+                       int n_kv_heads, int head_dim, int tp_degree, tp_bf16* ctx, void* workspace,
+                       size_t workspace_bytes, tp_stream_t stream) {
+  return run_tree<false>(qkv, k_cache, nullptr, v_cache, nullptr, tree_mask, T, past, max_len,
+                         n_q_heads, n_kv_heads, head_dim, tp_degree, ctx, workspace,
+                         workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tp_status tp_attn_decode_kv8(const tp_bf16* qkv, uint8_t* k_cache, float* k_scale, uint8_t* v_cache,
+                             float* v_scale, const uint64_t* tree_mask, int T, int past,
+                             int max_len, int n_q_heads, int n_kv_heads, int head_dim,
+                             int tp_degree, tp_bf16* ctx, void* workspace, size_t workspace_bytes,
+                             tp_stream_t stream) {
+  return run_tree<true>(qkv, k_cache, k_scale, v_cache, v_scale, tree_mask, T, past, max_len,
+                        n_q_heads, n_kv_heads, head_dim, tp_degree, ctx, workspace,
+                        workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 tp_status tp_colpar_gemm_gelu_w8(const tp_bf16* x, const uint8_t* w8, const float* w_scale,
