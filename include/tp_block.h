@@ -309,8 +309,8 @@ tp_status tp_attn_prefill(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache
  *             one exception to "outputs must not alias inputs"; the value heads
  *             are then not touched)
  * Requires d a multiple of 16 up to 256, rot_dim a multiple of 16 in [0, d],
- * nq a multiple of nkv, eps >= 0 (else TP_ERR_SHAPE); t dividing both head
- * counts.  One of gamma_q and gamma_k alone is TP_ERR_NULL.
+ * nq a multiple of nkv, nq + 2 nkv <= 4096, eps >= 0 (else TP_ERR_SHAPE); t
+ * dividing both head counts.  One of gamma_q and gamma_k alone is TP_ERR_NULL.
  */
 tp_status tp_qk_norm_rope(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf16* gamma_k,
                           const float* inv_freq, const int32_t* positions, int T, int past,

@@ -134,28 +134,18 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t: Optional[torch.Tensor], name: str, dev: torch.device) -> Optional[int]:
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    return _ptr_typed(t, name, dev, torch.bfloat16)
 
 
 def _ptr_typed(t: Optional[torch.Tensor], name: str, dev: torch.device,
                dtype: torch.dtype) -> Optional[int]:
-    """Like _ptr for the 8-bit weight bytes (uint8) and their fp32 scales."""
+    """The pointer of a contiguous tensor of the given type on the call's device."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if not t.is_contiguous():
@@ -178,7 +168,8 @@ def _device(t: torch.Tensor) -> torch.device:
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle itself: a torch.cuda.Stream object costs 3 us to build
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if stream.device.index != torch.cuda.current_device():
         raise ValueError(f"stream is on {stream.device}, not the current device")
     return stream.cuda_stream
@@ -500,27 +491,29 @@ def tp_sp_add_rmsnorm(y: torch.Tensor, residual: torch.Tensor, gamma: torch.Tens
     return r_out, n_out
 
 
-def _empty_on(shape, dtype: torch.dtype, dev: torch.device,
-              stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """An uninitialised tensor whose memory belongs to the call's stream: it is
-    handed out again only after the work enqueued there."""
+def _empty_on(like: torch.Tensor, shape, stream: Optional[torch.cuda.Stream],
+              dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """An uninitialised tensor on like's device (and of its type) whose memory
+    belongs to the call's stream: it is handed out again only after the work
+    enqueued there."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _workspace(workspace: Optional[torch.Tensor], need: int, dev: torch.device,
-               stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+def _workspace(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor,
+               dev: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """The caller's workspace, or one of `need` bytes (like is bf16)."""
     if workspace is None:
-        return _empty_on((max(need, 256),), torch.uint8, dev, stream)
+        return _empty_on(like, (max(need, 256) + 1) // 2, stream)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the same device")
     return workspace
 
 
 def _expect_shape(t: Optional[torch.Tensor], name: str, shape) -> None:
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -560,8 +553,9 @@ def tp_qk_norm_rope(qkv: torch.Tensor, past: int, n_q_heads: int, n_kv_heads: in
     gq, gk, fr, pos, rot = _qk_args(qkv, gamma_q, gamma_k, inv_freq, positions, n_q_heads,
                                     n_kv_heads, head_dim, dev)
     if out is None:
-        out = _empty_on(tuple(qkv.shape), torch.bfloat16, dev, stream)
-    _expect_shape(out, "out", qkv.shape)
+        out = _empty_on(qkv, qkv.shape, stream)
+    else:
+        _expect_shape(out, "out", qkv.shape)
     st = load().tp_qk_norm_rope(_ptr(qkv, "qkv", dev), gq, gk, fr, pos, qkv.shape[0], int(past),
                                 int(n_q_heads), int(n_kv_heads), int(head_dim), rot,
                                 _layout(layout), float(eps), int(tp_degree),
@@ -593,13 +587,14 @@ def tp_qk_norm_rope_backward(qkv: torch.Tensor, dout: torch.Tensor, past: int, n
     _expect_shape(dout, "dout", qkv.shape)
     T = qkv.shape[0]
     if dqkv is None:
-        dqkv = _empty_on(tuple(qkv.shape), torch.bfloat16, dev, stream)
-    _expect_shape(dqkv, "dqkv", qkv.shape)
+        dqkv = _empty_on(qkv, qkv.shape, stream)
+    else:
+        _expect_shape(dqkv, "dqkv", qkv.shape)
     dgq = dgk = ws = None
     if gq is not None:
-        dgq = _empty_on((head_dim,), torch.bfloat16, dev, stream)
-        dgk = _empty_on((head_dim,), torch.bfloat16, dev, stream)
-        ws = _workspace(workspace, tp_qk_norm_rope_backward_workspace_bytes(T, head_dim), dev,
+        dgq = _empty_on(qkv, head_dim, stream)
+        dgk = _empty_on(qkv, head_dim, stream)
+        ws = _workspace(workspace, tp_qk_norm_rope_backward_workspace_bytes(T, head_dim), qkv, dev,
                         stream)
     st = load().tp_qk_norm_rope_backward(
         _ptr(qkv, "qkv", dev), gq, gk, fr, pos, _ptr(dout, "dout", dev), T, int(past),
@@ -614,8 +609,9 @@ def tp_qk_norm_rope_backward(qkv: torch.Tensor, dout: torch.Tensor, past: int, n
 def _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim) -> None:
     if qkv.dim() != 2 or qkv.shape[1] != (n_q_heads + 2 * n_kv_heads) * head_dim:
         raise ValueError("qkv must be [T, (nq + 2 nkv) d]")
-    if k_cache.dim() != 3 or tuple(k_cache.shape) != tuple(v_cache.shape) or \
-            k_cache.shape[0] != n_kv_heads or k_cache.shape[2] != head_dim:
+    shape = k_cache.shape
+    if len(shape) != 3 or shape != v_cache.shape or shape[0] != n_kv_heads or \
+            shape[2] != head_dim:
         raise ValueError("caches must be [nkv, max_len, d]")
 
 
@@ -684,9 +680,9 @@ def tp_kv8_read(k_cache: torch.Tensor, k_scale: torch.Tensor, v_cache: torch.Ten
     if len(shape) != 3 or (shape[0], shape[2]) != (nkv, d):
         raise ValueError("k_out and v_out must be [nkv, out_len, d]")
     if k_out is None:
-        k_out = _empty_on(shape, torch.bfloat16, dev, stream)
+        k_out = _empty_on(k_cache, shape, stream, torch.bfloat16)
     if v_out is None:
-        v_out = _empty_on(shape, torch.bfloat16, dev, stream)
+        v_out = _empty_on(k_cache, shape, stream, torch.bfloat16)
     _expect_shape(v_out, "v_out", k_out.shape)
     _check(load().tp_kv8_read(*_kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev), int(start),
                               int(count), max_len, nkv, d, int(tp_degree),
@@ -718,11 +714,12 @@ def _tree_call(name, qkv, cache_ptrs, max_len, past, n_q_heads, n_kv_heads, head
     T = qkv.shape[0]
     _expect_shape(tree_mask, "tree_mask", (T, (T + 63) // 64))
     if ctx is None:
-        ctx = _empty_on((T, n_q_heads * head_dim), torch.bfloat16, dev, stream)
-    _expect_shape(ctx, "ctx", (T, n_q_heads * head_dim))
+        ctx = _empty_on(qkv, (T, n_q_heads * head_dim), stream)
+    else:
+        _expect_shape(ctx, "ctx", (T, n_q_heads * head_dim))
     workspace = _workspace(
-        workspace, tp_attn_tree_workspace_bytes(T, past, n_q_heads, n_kv_heads, head_dim), dev,
-        stream)
+        workspace, tp_attn_tree_workspace_bytes(T, past, n_q_heads, n_kv_heads, head_dim), qkv,
+        dev, stream)
     st = getattr(load(), name)(
         _ptr(qkv, "qkv", dev), *cache_ptrs, _ptr_typed(tree_mask, "tree_mask", dev, torch.int64), T,
         int(past), max_len, int(n_q_heads), int(n_kv_heads), int(head_dim), int(tp_degree),

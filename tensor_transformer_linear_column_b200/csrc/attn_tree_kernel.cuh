@@ -60,9 +60,13 @@ namespace tpb {
 constexpr int kTreeMaxTokens = 128;
 constexpr int kTreeStageBytes = 16384;  // one TMA item: 128 x 128 codes, or 16 KB of bf16
 constexpr int kTreeMaxStages = 8;
-constexpr float kLazyLog2 = 4.0f;
+// A weight may pass 1 by 2^16 over a bf16 cache: its relative error does not
+// depend on its size.  Over an 8-bit cache the terms of a weight end at 2^-17, so
+// the room above 1 is taken from the room below.
+constexpr float kLazyLog2 = 16.0f;
+constexpr float kLazyLog2Kv8 = 6.0f;
 constexpr float kUnsetMax = -1e30f;     // the running maximum before the first key
-constexpr int kWeightShift = 11;        // 8 bits: weights are split after times 2^11
+constexpr int kWeightShift = 9;         // 8 bits: weights are split after times 2^9
 
 struct TreeParams {
   int T, past, nq, nkv, G;
@@ -81,9 +85,13 @@ struct TreeParams {
 
 template <int kRows, bool k8>
 struct TreeShape {
-  static constexpr int kGroups = kRows >= 32 ? 2 : 1;      // softmax warpgroups
-  static constexpr int kCols = kRows / kGroups;            // query rows per thread
-  static constexpr int kThreads = 64 + 128 * kGroups;      // + TMA warp, MMA warp
+  static constexpr int kGroups = kRows >= 64 ? 4 : kRows / 16;  // softmax warpgroups
+  static constexpr int kCols = kRows / kGroups;                 // query rows per thread
+  // the TMA warp and the MMA warp; a whole warpgroup with them where registers
+  // are handed from it to the softmax warps
+  static constexpr bool kHandOver = false;
+  static constexpr int kFirst = kHandOver ? 4 : 2;
+  static constexpr int kThreads = 32 * kFirst + 128 * kGroups;
   static constexpr int kBlocksPerSm = kRows <= 32 ? 2 : 1;
   static constexpr int kKItems = k8 ? 1 : 2;               // stages per K (and per V) block
   static constexpr int kParts = k8 ? 3 : 1;                // weight operands
@@ -91,7 +99,7 @@ struct TreeShape {
   static constexpr int kSlotBytes = kParts * kPartBytes;
   static constexpr int kQBytes = 2 * kRows * 128;          // hi, lo; or the two d halves
   static constexpr int kTmemCols = kRows == 16 ? 64 : kRows == 32 ? 128 : kRows == 64 ? 256 : 512;
-  static constexpr int kSmallBytes = (4 * kRows + 4 * kRows) * 4 + 32 + 256;
+  static constexpr int kSmallBytes = (4 * kRows + 4 * kRows) * 4 + 64 + 256;
   static constexpr int kSmemTarget = kBlocksPerSm == 2 ? (228 * 1024) / 2 - 1024 : 227 * 1024;
   static constexpr int kFit = (kSmemTarget - 1024 - kSmallBytes - kQBytes - 2 * kSlotBytes) /
                               kTreeStageBytes;
@@ -265,14 +273,14 @@ __device__ __forceinline__ void append_rows(const TreeParams& p, int g, int part
 // 16 weights (already times 2^11 times the value scale over C) as three 16-byte
 // vectors of E5M2 terms: a = the leading 3 bits, b = the next of the rest, c =
 // the rest of that, rounded.  x - a and x - a - b are exact in fp16.
-__device__ __forceinline__ void split_weights(const float* w, uint4& a4, uint4& b4, uint4& c4) {
+__device__ __forceinline__ void split_weights(const float2* w, uint4& a4, uint4& b4, uint4& c4) {
   uint32_t a[4], b[4], c[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     uint32_t av[2], bv[2], cv[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const __half2 x = __floats2half2_rn(w[4 * q + 2 * h], w[4 * q + 2 * h + 1]);
+      const __half2 x = __float22half2_rn(w[2 * q + h]);
       const uint32_t xb = *reinterpret_cast<const uint32_t*>(&x);
       av[h] = xb & 0xFF00FF00u;
       const __half2 r1 = __hsub2(x, *reinterpret_cast<const __half2*>(&av[h]));
@@ -317,13 +325,13 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
   uint8_t* ring = smem;
   uint8_t* qs = ring + kStages * kTreeStageBytes;
   uint8_t* ps = qs + Sh::kQBytes;                                   // [2 slots][parts]
-  float* m_s = reinterpret_cast<float*>(ps + 2 * Sh::kSlotBytes);   // running maxima
-  float* a_s = m_s + kRows;      // this raise's factor of O
+  float* nm_s = reinterpret_cast<float*>(ps + 2 * Sh::kSlotBytes);  // minus the running maxima
+  float* a_s = nm_s + kRows;      // this raise's factor of O
   float* al_s = a_s + kRows;     // this raise's factor of the sums
   float* rf_s = al_s + kRows;    // 8 bits: score factor of each row
   float* red = rf_s + kRows;     // [4][kRows]
-  int* red_c = reinterpret_cast<int*>(red + 4 * kRows);  // [2 warpgroups][4]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(red_c + 8);
+  int* red_c = reinterpret_cast<int*>(red + 4 * kRows);  // [4 warpgroups][4]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(red_c + 16);
   uint64_t* full_bar = bars;                      // [kStages]
   uint64_t* empty_bar = full_bar + kTreeMaxStages;
   uint64_t* q_bar = empty_bar + kTreeMaxStages;   // the query operand is written
@@ -369,6 +377,15 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t o_col = 2u * kRows;  // score slots at columns 0 and kRows, then O
+
+  if constexpr (Sh::kHandOver) {
+    // 640 threads at 96 registers; 24 are enough for the two issuing threads,
+    // and 24 + 4 x 112 stay below 5 x 96
+    if (warp < Sh::kFirst)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+  }
 
   if (warp == 0) {
     if (lane == 0) {
@@ -506,13 +523,13 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       drain_wait(smem_u32(final_bar), 0, 50ull * 1000ull * 1000ull);
     }
     __syncwarp();
-  } else {
+  } else if (warp >= Sh::kFirst) {
     // ---------------- softmax warps.  Thread r of a warpgroup owns TMEM lane r:
     // key r of each block, and element r of O; warpgroup w owns query rows
     // [w kCols, (w + 1) kCols).  Every thread takes the same barriers and
     // arrivals whatever its waits returned.
     grid_dependency_wait();  // qkv; and the partials may still be read
-    const int st = threadIdx.x - 64;
+    const int st = threadIdx.x - 32 * Sh::kFirst;
     const int wg = st >> 7;
     const int et = st & 127;
     const int q4 = warp & 3;
@@ -526,75 +543,98 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(q_bar));
     append_rows<k8>(p, g, chunk + p.chunks * grp, p.chunks * p.groups, st, kSoftmax);
-    if (et < kCols) m_s[c0 + et] = kUnsetMax;
-    named_barrier_sync(3, kSoftmax);  // rf_s and m_s are written
+    if (et < kCols) nm_s[c0 + et] = -kUnsetMax;
+    named_barrier_sync(5, kSoftmax);  // rf_s and nm_s are written
 
-    float lsum[kCols];
+    float2 lsum[kCols / 2];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) lsum[j] = 0.0f;
+    for (int j = 0; j < kCols / 2; ++j) lsum[j] = make_float2(0.0f, 0.0f);
     int c_exp = -100;  // 8 bits: C = 2^c_exp
     bool ok = true;
+    const float* scale_k = nullptr;
+    const float* scale_v = nullptr;
+    float kscale = p.scale_log2, vscale = 0.0f, k_next = 0.0f, v_next = 0.0f;
+    if constexpr (k8) {
+      scale_k = p.cache_scale[0] + static_cast<size_t>(g) * p.max_len + key0 + r;
+      scale_v = p.cache_scale[1] + static_cast<size_t>(g) * p.max_len + key0 + r;
+      if (key0 + r < p.past) {
+        k_next = __ldg(scale_k);
+        v_next = __ldg(scale_v);
+      }
+    }
     for (int b = 0; b < nbc; ++b) {
       const int slot = b & 1;
-      const int key = key0 + b * 128 + r;
-      const bool valid = key < p.past;
-      float kscale = p.scale_log2, vscale = 0.0f;
+      const int left = p.past - (key0 + b * 128);  // keys from this block on
       if constexpr (k8) {
-        const size_t at = static_cast<size_t>(g) * p.max_len + key;
-        kscale = valid ? __ldg(p.cache_scale[0] + at) : 0.0f;
-        vscale = valid ? __ldg(p.cache_scale[1] + at) : 0.0f;
+        kscale = k_next;
+        vscale = v_next;
+        k_next = v_next = 0.0f;
+        if (b + 1 < nbc && r + 128 < left) {
+          k_next = __ldg(scale_k + (b + 1) * 128);
+          v_next = __ldg(scale_v + (b + 1) * 128);
+        }
       }
       ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&s_full[slot]), (b >> 1) & 1,
                                                      abort_flag));
       tc_fence_after();
-      uint32_t sv[kCols];
-      if (ok) {
-        tmem_ld_cols<kCols>(tmem + lane_addr + static_cast<uint32_t>(slot * kRows + c0), sv);
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) sv[j] = 0u;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s_free[slot]));
-      // t: scores in base-2 units; the running maximum stays unless some t
-      // passes it by more than kLazyLog2
-      float t[kCols];
+      const uint32_t s_at = tmem + lane_addr + static_cast<uint32_t>(slot * kRows + c0);
+      // e: scores in base-2 units over the running maximum, which stays unless
+      // some e passes kLazyLog2
+      float2 e[kCols / 2];
       float over = kUnsetMax;
+      auto scores = [&] {
+        uint32_t sv[kCols];
+        if (ok) {
+          tmem_ld_cols<kCols>(s_at, sv);
+          tmem_wait_ld();
+        } else {
 #pragma unroll
-      for (int j = 0; j < kCols; ++j) {
-        float f = kscale;
-        if constexpr (k8) f *= rf_s[c0 + j];
-        t[j] = valid ? __uint_as_float(sv[j]) * f : neg_inf();
-        over = fmaxf(over, t[j] - m_s[c0 + j]);
-      }
-      bool raise = b == 0 || over > kLazyLog2;
+          for (int j = 0; j < kCols; ++j) sv[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j)
+          e[j] = make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
+      };
+      auto factor = [&](int j) {
+        float2 f = make_float2(kscale, kscale);
+        if constexpr (k8) f = mul2(f, *reinterpret_cast<const float2*>(rf_s + c0 + 2 * j));
+        return f;
+      };
+      auto hide = [&] {  // keys behind the cache's last, in its last block
+        if (left < 128 && r >= left) {
+#pragma unroll
+          for (int j = 0; j < kCols / 2; ++j) e[j] = make_float2(neg_inf(), neg_inf());
+        }
+      };
+      auto excess = [&] {
+        scores();
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j)
+          e[j] = fma2(e[j], factor(j), *reinterpret_cast<const float2*>(nm_s + c0 + 2 * j));
+        hide();
+      };
+      excess();
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) over = fmaxf(over, fmaxf(e[j].x, e[j].y));
+      bool raise = over > (k8 ? kLazyLog2Kv8 : kLazyLog2);
       if constexpr (k8) raise = raise || vscale > pow2i(c_exp);
-      raise = named_barrier_any(bar_id, 128, raise);
-      if (raise) {
+      if (named_barrier_any(bar_id, 128, raise)) {
         // the block's maximum of every row (and of the value scales), over the
         // lanes of a warp and then the four warps in order
+        scores();
 #pragma unroll
-        for (int c = 0; c < kCols; c += (kCols == 16 ? 16 : 32)) {
-          if constexpr (kCols == 16) {
-            float mx[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) mx[j] = t[j];
-            const float m = warp_rows_reduce<16, true>(mx, lane);
-            if ((lane & 1) == 0) red[q4 * kRows + c0 + ((lane >> 1) & 15)] = m;
-          } else {
-            float mx[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx[j] = t[c + j];
-            const float m = warp_rows_reduce<32, true>(mx, lane);
-            red[q4 * kRows + c0 + c + lane] = m;
-          }
+        for (int j = 0; j < kCols / 2; ++j) e[j] = mul2(e[j], factor(j));
+        hide();
+        {
+          const float m =
+              warp_rows_reduce<kCols, true>(*reinterpret_cast<float(*)[kCols]>(e), lane);
+          if (kCols == 32 || (lane & 1) == 0)
+            red[q4 * kRows + c0 + (kCols == 32 ? lane : (lane >> 1) & 15)] = m;
         }
         int c_new = c_exp;
         if constexpr (k8) {
-          const int e = __reduce_max_sync(0xffffffffu, scale_exponent(vscale));
-          if (lane == 0) red_c[wg * 4 + q4] = e;
+          const int ce = __reduce_max_sync(0xffffffffu, scale_exponent(vscale));
+          if (lane == 0) red_c[wg * 4 + q4] = ce;
         }
         named_barrier_sync(bar_id, 128);
         if constexpr (k8) {
@@ -603,18 +643,20 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
         }
         if (et < kCols) {
           const int n = c0 + et;
-          const float mo = m_s[n];
+          const float mo = -nm_s[n];
           float mn = fmaxf(fmaxf(red[n], red[kRows + n]), fmaxf(red[2 * kRows + n], red[3 * kRows + n]));
           mn = fmaxf(mo, mn);
           const float al = exp2f(mo - mn);
-          m_s[n] = mn;
+          nm_s[n] = -mn;
           al_s[n] = al;
           a_s[n] = k8 ? al * pow2i(c_exp - c_new < -126 ? -126 : c_exp - c_new) : al;
         }
         c_exp = c_new;
         named_barrier_sync(bar_id, 128);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) lsum[j] *= al_s[c0 + j];
+        for (int j = 0; j < kCols / 2; ++j)
+          lsum[j] = mul2(lsum[j], *reinterpret_cast<const float2*>(al_s + c0 + 2 * j));
+        excess();
         if (b > 0) {
           // O holds the products of blocks 0 .. b - 1: wait for the last
           ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[slot ^ 1]),
@@ -636,21 +678,24 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
           }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s_free[slot]));
       // the slot's weights are free once block b - 2's value product is done
       if (b >= 2)
         ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[slot]),
                                                        ((b - 2) >> 1) & 1, abort_flag));
       uint8_t* pslot = ps + slot * Sh::kSlotBytes;
-      float wf = 1.0f;
-      if constexpr (k8) wf = vscale * pow2i(kWeightShift - c_exp);
+      float2 wf = make_float2(1.0f, 1.0f);
+      if constexpr (k8) wf.x = wf.y = vscale * pow2i(kWeightShift - c_exp);
 #pragma unroll
       for (int c = 0; c < kCols; c += 16) {
-        float w[16];
+        float2 w[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float e = exp2_fast(t[c + j] - m_s[c0 + c + j]);
-          lsum[c + j] += e;
-          w[j] = k8 ? e * wf : e;
+        for (int j = 0; j < 8; ++j) {
+          w[j] = make_float2(exp2_fast(e[c / 2 + j].x), exp2_fast(e[c / 2 + j].y));
+          lsum[c / 2 + j] = add2(lsum[c / 2 + j], w[j]);
+          if constexpr (k8) w[j] = mul2(w[j], wf);
         }
         if constexpr (k8) {
           uint4 a4, b4, c4;
@@ -663,10 +708,10 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             *reinterpret_cast<uint4*>(pslot + ((c0 + c) / 8 + h) * 2048 + r * 16) =
-                make_uint4(pack_bf16x2(w[8 * h], w[8 * h + 1]),
-                           pack_bf16x2(w[8 * h + 2], w[8 * h + 3]),
-                           pack_bf16x2(w[8 * h + 4], w[8 * h + 5]),
-                           pack_bf16x2(w[8 * h + 6], w[8 * h + 7]));
+                make_uint4(pack_bf16x2(w[4 * h].x, w[4 * h].y),
+                           pack_bf16x2(w[4 * h + 1].x, w[4 * h + 1].y),
+                           pack_bf16x2(w[4 * h + 2].x, w[4 * h + 2].y),
+                           pack_bf16x2(w[4 * h + 3].x, w[4 * h + 3].y));
         }
       }
       fence_proxy_async_smem();  // the weights are read by the MMA through the async proxy
@@ -675,22 +720,17 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       if (lane == 0) mbar_arrive(smem_u32(&p_full[slot]));
     }
     // the rows' sums over the lanes, then the four warps in order
-#pragma unroll
-    for (int c = 0; c < kCols; c += (kCols == 16 ? 16 : 32)) {
-      if constexpr (kCols == 16) {
-        const float v = warp_rows_reduce<16, false>(lsum, lane);
-        if ((lane & 1) == 0) red[q4 * kRows + c0 + ((lane >> 1) & 15)] = v;
-      } else {
-        const float v =
-            warp_rows_reduce<32, false>(*reinterpret_cast<float(*)[32]>(lsum + c), lane);
-        red[q4 * kRows + c0 + c + lane] = v;
-      }
+    {
+      const float v =
+          warp_rows_reduce<kCols, false>(*reinterpret_cast<float(*)[kCols]>(lsum), lane);
+      if (kCols == 32 || (lane & 1) == 0)
+        red[q4 * kRows + c0 + (kCols == 32 ? lane : (lane >> 1) & 15)] = v;
     }
     named_barrier_sync(bar_id, 128);
     const size_t part = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks + chunk;
     if (et < kCols && row0 + c0 + et < p.R) {
       const int n = c0 + et;
-      float2 ml = make_float2(m_s[n], ((red[n] + red[kRows + n]) + red[2 * kRows + n]) +
+      float2 ml = make_float2(-nm_s[n], ((red[n] + red[kRows + n]) + red[2 * kRows + n]) +
                                           red[3 * kRows + n]);
       *reinterpret_cast<float2*>(p.part_ml + (part * kRows + n) * 2) = ml;
     }

@@ -122,6 +122,9 @@ constexpr TreeLaunch tree_launch() {
   return TreeLaunch{tpb::attn_tree_kernel<kRows, k8>, kRows, Sh::kThreads, Sh::kSmem,
                     Sh::kBlocksPerSm};
 }
+using QkKernel = void (*)(const tpb::QkParams);
+QkKernel qk_kernel(int lanes, int layout, bool backward);
+
 const TreeLaunch kTreeLaunches[2][4] = {
     {tree_launch<16, false>(), tree_launch<32, false>(), tree_launch<64, false>(),
      tree_launch<128, false>()},
@@ -191,6 +194,17 @@ const DeviceInfo* device_info() {
                                         cudaSharedmemCarveoutMaxShared),
                    "cudaFuncSetAttribute"))
         return nullptr;
+  for (int lanes = 2; lanes <= 32; lanes *= 2)
+    for (int variant = 0; variant < 4; ++variant) {
+      QkKernel k = qk_kernel(lanes, variant & 1 ? TP_ROPE_PAIRS : TP_ROPE_HALF, (variant & 2) != 0);
+      if (!cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        tpb::kQkStages * tpb::kQkSlotBytes),
+                   "cudaFuncSetAttribute") ||
+          !cuda_ok(cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                        cudaSharedmemCarveoutMaxShared),
+                   "cudaFuncSetAttribute"))
+        return nullptr;
+    }
   d.sms = sms;
   d.max_smem = smem;
   d.ready = true;
@@ -736,7 +750,7 @@ tp_status check_qk(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf16* ga
     return TP_ERR_ALIGN;
   if (!heads_ok(T, past, nq, nkv) || !row_dim_ok(d) || rot < 0 || rot > d || rot % 16 != 0 ||
       !(eps >= 0.0f) || static_cast<long long>(past) + T > INT_MAX ||
-      static_cast<long long>(nq) + 2ll * nkv > (1 << 20))
+      static_cast<long long>(nq) + 2ll * nkv > tpb::kQkMaxHeads)
     return TP_ERR_SHAPE;
   if (layout != TP_ROPE_HALF && layout != TP_ROPE_PAIRS) return TP_ERR_UNSUPPORTED;
   if (t < 1 || nq % t != 0 || nkv % t != 0) return TP_ERR_TP_DEGREE;
@@ -745,8 +759,7 @@ tp_status check_qk(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf16* ga
 
 tpb::QkParams qk_params(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf16* gamma_k,
                         const float* inv_freq, const int* positions, int T, int past, int nq,
-                        int nkv, int d, int rot, int layout, float eps, tp_bf16* out,
-                        bool in_place) {
+                        int nkv, int d, int rot, float eps, tp_bf16* out, bool in_place) {
   tpb::QkParams p{};
   p.x = qkv;
   p.gamma_q = gamma_q;
@@ -760,16 +773,51 @@ tpb::QkParams qk_params(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_bf1
   p.nkv = nkv;
   p.d = d;
   p.rot = rot;
-  p.lanes = row_lanes(d);
   p.heads = nq + (in_place ? 1 : 2) * nkv;
-  p.pairs = layout == TP_ROPE_PAIRS ? 1 : 0;
   p.eps = eps;
   return p;
 }
 
-// Blocks of the gradient kernel: a function of T only, so the gains' sums are
-// taken in the same order on every device.
-int qk_backward_blocks(int T) { return T < tpb::kQkMaxBlocks ? T : tpb::kQkMaxBlocks; }
+// The instantiation for `lanes` lanes per head (2, 4, 8, 16, 32).
+QkKernel qk_kernel(int lanes, int layout, bool backward) {
+#define TP_QK(L)                                                                          \
+  (backward ? (layout == TP_ROPE_PAIRS ? tpb::qk_norm_rope_kernel<L, true, true>          \
+                                       : tpb::qk_norm_rope_kernel<L, false, true>)        \
+            : (layout == TP_ROPE_PAIRS ? tpb::qk_norm_rope_kernel<L, true, false>         \
+                                       : tpb::qk_norm_rope_kernel<L, false, false>))
+  switch (lanes) {
+    case 2: return TP_QK(2);
+    case 4: return TP_QK(4);
+    case 8: return TP_QK(8);
+    case 16: return TP_QK(16);
+    default: return TP_QK(32);
+  }
+#undef TP_QK
+}
+
+// Heads per segment: whole tokens where they fit a slot, and few enough that few
+// tokens reach every block.  The grid (tokens' blocks, segments) is a function
+// of the sizes only, so the gains' sums are taken in the same order everywhere.
+dim3 plan_qk(tpb::QkParams& p, bool backward) {
+  const int step = tpb::kQkWarps * 32 / row_lanes(p.d);  // heads a block holds at once
+  int seg = tpb::kQkSlotBytes / (p.d * (backward ? 4 : 2));
+  const long long spread = (static_cast<long long>(p.T) * p.heads + tpb::kQkMaxBlocks - 1) /
+                           tpb::kQkMaxBlocks;
+  if (spread < seg) seg = static_cast<int>(spread < step ? step : spread);
+  if (seg > p.heads) seg = p.heads;
+  const int segs = (p.heads + seg - 1) / seg;
+  p.seg = (p.heads + segs - 1) / segs;  // segments of a token alike
+  int x = tpb::kQkMaxBlocks / segs;
+  x = x < 1 ? 1 : x > p.T ? p.T : x;
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>((p.heads + p.seg - 1) / p.seg), 1);
+}
+
+// Ring bytes of a launch; the gradient's last step needs 8 floats a thread.
+int qk_smem(const tpb::QkParams& p, bool backward) {
+  const int ring = tpb::kQkStages * p.seg * p.d * (backward ? 4 : 2);
+  const int share = tpb::kQkWarps * 32 * 8 * 4;
+  return backward && ring < share ? share : ring;
+}
 
 cudaLaunchConfig_t launch_config(dim3 grid, int threads, int smem, cudaStream_t stream,
                                  cudaLaunchAttribute* attr) {
@@ -1327,27 +1375,23 @@ tp_status tp_qk_norm_rope(const tp_bf16* qkv, const tp_bf16* gamma_q, const tp_b
                                n_kv_heads, head_dim, rot_dim, layout, eps, tp_degree);
   if (s != TP_OK) return s;
   tpb::QkParams p = qk_params(qkv, gamma_q, gamma_k, inv_freq, positions, T, past, n_q_heads,
-                              n_kv_heads, head_dim, rot_dim, layout, eps, out, out == qkv);
-  // one block holds 8 x 32 / lanes heads at a time; few tokens share their
-  // heads among blocks until about two blocks per SM have work
-  const int step = tpb::kQkThreads / p.lanes;
-  const int most = (p.heads + step - 1) / step;
-  p.slices = T >= 296 ? 1 : (296 + T - 1) / T;
-  p.slices = p.slices > most ? most : p.slices;
-  if (static_cast<long long>(T) * p.slices > INT_MAX) return TP_ERR_SHAPE;
+                              n_kv_heads, head_dim, rot_dim, eps, out, out == qkv);
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return TP_ERR_CUDA;
+  const dim3 grid = plan_qk(p, false);
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = launch_config(dim3(static_cast<unsigned>(T * p.slices), 1, 1),
-                                         tpb::kQkThreads, 0,
-                                         reinterpret_cast<cudaStream_t>(stream), attr);
-  return cuda_ok(cudaLaunchKernelEx(&cfg, tpb::qk_norm_rope_kernel, p), "launch qk_norm_rope_kernel")
+  cudaLaunchConfig_t cfg =
+      launch_config(grid, tpb::kQkThreads, qk_smem(p, false),
+                    reinterpret_cast<cudaStream_t>(stream), attr);
+  return cuda_ok(cudaLaunchKernelEx(&cfg, qk_kernel(row_lanes(head_dim), layout, false), p),
+                 "launch qk_norm_rope_kernel")
              ? TP_OK
              : TP_ERR_CUDA;
 }
 
 size_t tp_qk_norm_rope_backward_workspace_bytes(int T, int head_dim) {
   if (T < 1 || !row_dim_ok(head_dim)) return 0;
-  return (static_cast<size_t>(qk_backward_blocks(T)) * 2u * static_cast<size_t>(head_dim) * 4u +
-          255u) / 256u * 256u;
+  return static_cast<size_t>(tpb::kQkMaxBlocks) * 2u * static_cast<size_t>(head_dim) * 4u;
 }
 
 tp_status tp_qk_norm_rope_backward(const tp_bf16* qkv, const tp_bf16* gamma_q,
@@ -1373,15 +1417,18 @@ tp_status tp_qk_norm_rope_backward(const tp_bf16* qkv, const tp_bf16* gamma_q,
     if (!aligned16(workspace)) return TP_ERR_ALIGN;
   }
   tpb::QkParams p = qk_params(qkv, gamma_q, gamma_k, inv_freq, positions, T, past, n_q_heads,
-                              n_kv_heads, head_dim, rot_dim, layout, eps, dqkv, dqkv == dout);
+                              n_kv_heads, head_dim, rot_dim, eps, dqkv, dqkv == dout);
   p.dy = dout;
   p.partial = static_cast<float*>(workspace);
-  const int blocks = qk_backward_blocks(T);
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return TP_ERR_CUDA;
+  const dim3 grid = plan_qk(p, true);
+  const int blocks = static_cast<int>(grid.x * grid.y);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg =
-      launch_config(dim3(static_cast<unsigned>(blocks), 1, 1), tpb::kQkThreads, 0, st, attr);
-  if (!cuda_ok(cudaLaunchKernelEx(&cfg, tpb::qk_norm_rope_backward_kernel, p),
+      launch_config(grid, tpb::kQkThreads, qk_smem(p, true), st, attr);
+  if (!cuda_ok(cudaLaunchKernelEx(&cfg, qk_kernel(row_lanes(head_dim), layout, true), p),
                "launch qk_norm_rope_backward_kernel"))
     return TP_ERR_CUDA;
   if (!norm) return TP_OK;

@@ -37,7 +37,7 @@ QK_BAD = [
     (S, dict(T=0)), (S, dict(past=-1)), (S, dict(nq=0)), (S, dict(nkv=0)), (S, dict(nq=7)),
     (S, dict(d=0)), (S, dict(d=120)), (S, dict(d=272)), (S, dict(rot=-16)), (S, dict(rot=8)),
     (S, dict(rot=144)), (S, dict(eps=-1.0)), (S, dict(eps=float("nan"))),
-    (S, dict(past=BIG)), (S, dict(nq=1 << 30, nkv=1 << 29)),
+    (S, dict(past=BIG)), (S, dict(nq=1 << 30, nkv=1 << 29)), (S, dict(nq=4092, nkv=4)),
     (U, dict(layout=2)), (U, dict(layout=-1)), (D, dict(t=0)), (D, dict(t=4)), (D, dict(t=3)),
 ]
 
@@ -56,7 +56,7 @@ BACK_GOOD = dict({k: v for k, v in QK_GOOD.items() if k != "out"}, dout=GOOD, dq
     (N, dict(dout=None)), (N, dict(dqkv=None)), (N, dict(dgq=None)), (N, dict(dgk=None)),
     (A, dict(dout=ODD)), (A, dict(dqkv=ODD)), (A, dict(dgq=ODD)), (A, dict(dgk=ODD)),
     (A, dict(ws=ODD)), (W, dict(ws=None)), (W, dict(bytes=0)),
-    (W, dict(bytes=4 * 2 * 128 * 4 - 1)),
+    (W, dict(bytes=296 * 2 * 128 * 4 - 1)),
 ])
 def test_qk_norm_rope_backward(lib, status, change):
     assert _call(lib, "tp_qk_norm_rope_backward", BACK, BACK_GOOD, **change) == status
@@ -64,8 +64,8 @@ def test_qk_norm_rope_backward(lib, status, change):
 
 def test_qk_backward_workspace():
     f = tp.tp_qk_norm_rope_backward_workspace_bytes
-    assert f(4, 128) == 4 * 2 * 128 * 4
-    assert f(10 ** 6, 16) == f(10 ** 5, 16) > 0  # bounded in T
+    assert f(4, 128) == 296 * 2 * 128 * 4
+    assert f(1, 16) == f(10 ** 6, 16) == 296 * 2 * 16 * 4  # whatever T is
     assert f(0, 128) == f(4, 120) == f(4, 0) == f(4, 272) == 0
 
 

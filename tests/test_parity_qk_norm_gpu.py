@@ -51,7 +51,7 @@ SHAPES = [
     # T, nq, nkv, d, rot
     (1, 64, 8, 128, 128), (5, 64, 8, 128, 64), (3, 9, 3, 80, 32), (2, 4, 4, 16, 16),
     (7, 6, 2, 96, 96), (4, 3, 1, 256, 256), (300, 8, 2, 128, 128), (1, 1, 1, 64, 0),
-    (2, 130, 2, 112, 16), (601, 2, 1, 48, 48),
+    (2, 130, 2, 112, 16), (601, 2, 1, 48, 48), (3, 4000, 40, 16, 16), (2, 1998, 999, 256, 32),
 ]
 
 
