@@ -64,13 +64,14 @@ constexpr int kTreeMaxStages = 8;
 // depend on its size.  Over an 8-bit cache the terms of a weight end at 2^-17, so
 // the room above 1 is taken from the room below.
 constexpr float kLazyLog2 = 16.0f;
-constexpr float kLazyLog2Kv8 = 6.0f;
+constexpr float kLazyLog2Kv8 = 10.0f;
 constexpr float kUnsetMax = -1e30f;     // the running maximum before the first key
-constexpr int kWeightShift = 9;         // 8 bits: weights are split after times 2^9
+constexpr int kWeightShift = 5;         // 8 bits: weights are split after times 2^5
 
 struct TreeParams {
   int T, past, nq, nkv, G;
   int R;            // query rows per key-value head: T G
+  unsigned g_magic; // ceil(2^32 / G), G > 1: r / G is the upper word of r g_magic, r < 2^16
   int groups;       // row groups of kRows: grid z
   int nblk;         // key blocks of 128 in [0, past)
   int nb, chunks;   // key blocks per chunk, chunks per key-value head: grid x
@@ -85,20 +86,16 @@ struct TreeParams {
 
 template <int kRows, bool k8>
 struct TreeShape {
-  static constexpr int kGroups = kRows >= 64 ? 4 : kRows / 16;  // softmax warpgroups
-  static constexpr int kCols = kRows / kGroups;                 // query rows per thread
-  // the TMA warp and the MMA warp; a whole warpgroup with them where registers
-  // are handed from it to the softmax warps
-  static constexpr bool kHandOver = false;
-  static constexpr int kFirst = kHandOver ? 4 : 2;
-  static constexpr int kThreads = 32 * kFirst + 128 * kGroups;
+  static constexpr int kGroups = kRows / 16;  // softmax warpgroups
+  static constexpr int kCols = 16;            // query rows per thread
+  static constexpr int kThreads = 64 + 128 * kGroups;           // + TMA warp, MMA warp
   static constexpr int kBlocksPerSm = kRows <= 32 ? 2 : 1;
   static constexpr int kKItems = k8 ? 1 : 2;               // stages per K (and per V) block
   static constexpr int kParts = k8 ? 3 : 1;                // weight operands
   static constexpr int kPartBytes = 128 * kRows * (k8 ? 1 : 2);
   static constexpr int kSlotBytes = kParts * kPartBytes;
   static constexpr int kQBytes = 2 * kRows * 128;          // hi, lo; or the two d halves
-  static constexpr int kTmemCols = kRows == 16 ? 64 : kRows == 32 ? 128 : kRows == 64 ? 256 : 512;
+  static constexpr int kTmemCols = kRows == 16 ? 64 : kRows == 32 ? 128 : 256;
   static constexpr int kSmallBytes = (4 * kRows + 4 * kRows) * 4 + 64 + 256;
   static constexpr int kSmemTarget = kBlocksPerSm == 2 ? (228 * 1024) / 2 - 1024 : 227 * 1024;
   static constexpr int kFit = (kSmemTarget - 1024 - kSmallBytes - kQBytes - 2 * kSlotBytes) /
@@ -121,10 +118,10 @@ __device__ __forceinline__ uint64_t desc_mnmajor_plain(uint32_t saddr, uint32_t 
   return d;
 }
 
-// Instruction descriptor, kind::f8f6f4: E4M3 A, fp32 D; B is E4M3 or E5M2.
-__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool b_e5m2, bool a_mn,
-                                                    bool b_mn) {
-  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+// Instruction descriptor, kind::f8f6f4: fp32 D; A and B are E4M3 or E5M2.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool a_e5m2, bool b_e5m2,
+                                                    bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
@@ -171,62 +168,86 @@ __device__ __forceinline__ float pow2i(int e) {  // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Query rows [row0, row0 + kRows) of head g into shared memory as the K-major B
-// operand, by the softmax threads (16 lanes a row): bf16 as two 64-wide
-// halves, or the 8-bit hi / lo parts with each row's factor in rf_s.  Rows at
-// or past R are zero.
-template <int kRows, bool k8>
+// Two E4M3 codes of an fp16 pair, and back (exact).
+__device__ __forceinline__ uint32_t e4m3x2_of(uint32_t h2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of_e4m3x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+
+// Query rows [row0, row0 + kRows) of head g into shared memory as a K-major
+// operand, by kThreads threads (16 lanes a row): bf16 as two 64-wide halves, or
+// the 8-bit hi / lo parts with each row's factor in rf_s.  Rows at or past R are
+// zero.  Up to four rows a thread in flight and rolled beyond that: a block runs
+// this once, and each instruction line it has to fetch costs more than the loop
+// (128 rows unrolled: 10,000 cycles, 16,000 in 8 bits).
+template <int kRows, bool k8, int kThreads>
 __device__ __forceinline__ void load_queries(const TreeParams& p, int g, int row0, uint8_t* qs,
-                                             float* rf_s, int st, int nthreads) {
+                                             float* rf_s, int st) {
   const int l = st & 15;
-  for (int r = st >> 4; r < kRows; r += nthreads >> 4) {
-    const int rr = row0 + r;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (rr < p.R) {
-      const int tok = rr / p.G, h = g * p.G + rr % p.G;
-      raw = __ldg(reinterpret_cast<const uint4*>(
-                      p.qkv + (static_cast<size_t>(tok) * (p.nq + 2 * p.nkv) + h) * kAttnHeadDim) +
-                  l);
-    }
-    if constexpr (!k8) {
-      // half l / 8, 16-byte chunk l % 8 of the 128-byte row, swizzled
-      *reinterpret_cast<uint4*>(qs + (l >> 3) * (kRows * 128) + r * 128 +
-                                (((l & 7) ^ (r & 7)) << 4)) = raw;
-    } else {
-      float x[8];
-      unpack8(raw, x);
-      float amax = abs_max8(x);
+  constexpr int kPasses = kRows * 16 / kThreads;
+  constexpr int kFlight = kPasses < 4 ? kPasses : 4;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kPasses; i0 += kFlight) {
+    uint4 all[kFlight];
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      // shift: amax 2^shift in (224, 448]
-      const uint32_t bits = __float_as_uint(amax);
-      int shift = 8 - (static_cast<int>(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-      shift = amax > 0.0f ? (shift > 126 ? 126 : shift) : 0;
-      const float up = pow2i(shift);  // at least -120
-      float hi_f[8];
-      uint2 hi, lo;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] *= up;
-      hi = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t w = k < 2 ? hi.x : hi.y;
-        const __half2 h2(__nv_cvt_fp8x2_to_halfraw2(
-            static_cast<__nv_fp8x2_storage_t>(w >> (16 * (k & 1))), __NV_E4M3));
-        const float2 f = __half22float2(h2);
-        hi_f[2 * k] = f.x;
-        hi_f[2 * k + 1] = f.y;
+    for (int i = 0; i < kFlight; ++i) {
+      const int rr = row0 + (st >> 4) + (i0 + i) * (kThreads >> 4);
+      all[i] = make_uint4(0, 0, 0, 0);
+      if (rr < p.R) {
+        const int tok =
+            p.G == 1 ? rr : static_cast<int>(__umulhi(static_cast<unsigned>(rr), p.g_magic));
+        const int h = g * p.G + rr - tok * p.G;
+        all[i] = __ldg(reinterpret_cast<const uint4*>(
+                           p.qkv +
+                           (static_cast<size_t>(tok) * (p.nq + 2 * p.nkv) + h) * kAttnHeadDim) +
+                       l);
       }
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] -= hi_f[k];  // exact: the low bits of x
-      lo = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
-      const int off = r * 128 + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8;
-      *reinterpret_cast<uint2*>(qs + off) = hi;
-      *reinterpret_cast<uint2*>(qs + kRows * 128 + off) = lo;
-      // a row that holds an infinity scores NaN (its parts are clamped)
-      if (l == 0)
-        rf_s[r] = amax > 3.3895314e38f ? __int_as_float(0x7fc00000)
-                                       : p.scale_log2 * pow2i(-shift);
+    for (int i = 0; i < kFlight; ++i) {
+      const int r = (st >> 4) + (i0 + i) * (kThreads >> 4);
+      const uint4 raw = all[i];
+      if constexpr (!k8) {
+        // half l / 8, 16-byte chunk l % 8 of the 128-byte row, swizzled
+        *reinterpret_cast<uint4*>(qs + (l >> 3) * (kRows * 128) + r * 128 +
+                                  (((l & 7) ^ (r & 7)) << 4)) = raw;
+      } else {
+        float x[8];
+        unpack8(raw, x);
+        float amax = abs_max8(x);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // shift: amax 2^shift in (224, 448]
+        const uint32_t bits = __float_as_uint(amax);
+        int shift =
+            8 - (static_cast<int>(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        shift = amax > 0.0f ? (shift > 126 ? 126 : shift) : 0;
+        const float up = pow2i(shift);  // at least -120
+        // in fp16 the scaled elements are exact down to 2^-14, as hi and the rest
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 v = __floats2half2_rn(x[2 * k] * up, x[2 * k + 1] * up);
+          hi[k] = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&v));
+          const uint32_t back = half2_of_e4m3x2(hi[k]);
+          const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
+          lo[k] = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&rest));
+        }
+        const int off = r * 128 + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8;
+        *reinterpret_cast<uint2*>(qs + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+        *reinterpret_cast<uint2*>(qs + kRows * 128 + off) =
+            make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        // a row that holds an infinity scores NaN (its parts are clamped)
+        if (l == 0)
+          rf_s[r] = amax > 3.3895314e38f ? __int_as_float(0x7fc00000)
+                                         : p.scale_log2 * pow2i(-shift);
+      }
     }
   }
 }
@@ -237,22 +258,22 @@ template <bool k8>
 __device__ __forceinline__ void append_rows(const TreeParams& p, int g, int part, int parts, int st,
                                             int nthreads) {
   const int l = st & 15;
-  const int per_pass = nthreads >> 4;
-  for (int base = 0; base < 2 * p.T; base += parts * per_pass) {
+#pragma unroll 1
+  for (int base = 0; base < 2 * p.T; base += parts * (nthreads >> 4)) {
     const int item = base + (st >> 4) * parts + part;  // (token, K or V)
     const bool in = item < 2 * p.T;
-    const int tok = item >> 1, which = item & 1;
+    if (!__any_sync(0xffffffffu, in)) continue;
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (in)
       raw = __ldg(reinterpret_cast<const uint4*>(
-                      p.qkv + (static_cast<size_t>(tok) * (p.nq + 2 * p.nkv) + p.nq +
-                               which * p.nkv + g) * kAttnHeadDim) +
+                      p.qkv + (static_cast<size_t>(item >> 1) * (p.nq + 2 * p.nkv) + p.nq +
+                               (item & 1) * p.nkv + g) * kAttnHeadDim) +
                   l);
-    const size_t row = static_cast<size_t>(g) * p.max_len + p.past + tok;
+    const size_t row = static_cast<size_t>(g) * p.max_len + p.past + (item >> 1);
+    void* cache = item & 1 ? p.cache[1] : p.cache[0];
     if constexpr (!k8) {
       if (in)
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>((which ? p.cache[1] : p.cache[0])) + row * kAttnHeadDim)[l] =
-            raw;
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + row * kAttnHeadDim)[l] = raw;
     } else {
       float x[8];
       unpack8(raw, x);
@@ -262,9 +283,8 @@ __device__ __forceinline__ void append_rows(const TreeParams& p, int g, int part
       float scale;
       const uint2 codes = kv8_codes(x, amax, scale);
       if (in) {
-        reinterpret_cast<uint2*>(static_cast<uint8_t*>((which ? p.cache[1] : p.cache[0])) + row * kAttnHeadDim)[l] =
-            codes;
-        if (l == 0) (which ? p.cache_scale[1] : p.cache_scale[0])[row] = scale;
+        reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * kAttnHeadDim)[l] = codes;
+        if (l == 0) (item & 1 ? p.cache_scale[1] : p.cache_scale[0])[row] = scale;
       }
     }
   }
@@ -296,18 +316,6 @@ __device__ __forceinline__ void split_weights(const float2* w, uint4& a4, uint4&
   a4 = make_uint4(a[0], a[1], a[2], a[3]);
   b4 = make_uint4(b[0], b[1], b[2], b[3]);
   c4 = make_uint4(c[0], c[1], c[2], c[3]);
-}
-
-// TMEM columns [col, col + kCols) of this thread's lane.
-template <int kCols>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&v)[kCols]) {
-  if constexpr (kCols == 16) {
-    tmem_ld16(addr, v);
-  } else {
-#pragma unroll
-    for (int c = 0; c < kCols; c += 32)
-      tmem_ld32(addr + static_cast<uint32_t>(c), *reinterpret_cast<uint32_t(*)[32]>(v + c));
-  }
 }
 
 template <int kRows, bool k8>
@@ -377,15 +385,6 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t o_col = 2u * kRows;  // score slots at columns 0 and kRows, then O
-
-  if constexpr (Sh::kHandOver) {
-    // 640 threads at 96 registers; 24 are enough for the two issuing threads,
-    // and 24 + 4 x 112 stay below 5 x 96
-    if (warp < Sh::kFirst)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-  }
 
   if (warp == 0) {
     if (lane == 0) {
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
             tc_fence_after();
             const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
             if constexpr (k8) {
-              constexpr uint32_t idesc = idesc_f8_f32(128, kRows, false, false, false);
+              constexpr uint32_t idesc = idesc_f8_f32(128, kRows, false, false, false, false);
 #pragma unroll
               for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -492,7 +491,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
             const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
             if constexpr (k8) {
               // 32 keys a step: V 4096 bytes on, the weights 4 core matrices on
-              constexpr uint32_t idesc = idesc_f8_f32(128, kRows, true, true, true);
+              constexpr uint32_t idesc = idesc_f8_f32(128, kRows, false, true, true, true);
 #pragma unroll
               for (int part = 0; part < 3; ++part)
 #pragma unroll
@@ -523,13 +522,14 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       drain_wait(smem_u32(final_bar), 0, 50ull * 1000ull * 1000ull);
     }
     __syncwarp();
-  } else if (warp >= Sh::kFirst) {
+  } else {
     // ---------------- softmax warps.  Thread r of a warpgroup owns TMEM lane r:
     // key r of each block, and element r of O; warpgroup w owns query rows
     // [w kCols, (w + 1) kCols).  Every thread takes the same barriers and
     // arrivals whatever its waits returned.
     grid_dependency_wait();  // qkv; and the partials may still be read
-    const int st = threadIdx.x - 32 * Sh::kFirst;
+    grid_launch_dependents();
+    const int st = threadIdx.x - 64;
     const int wg = st >> 7;
     const int et = st & 127;
     const int q4 = warp & 3;
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     const uint32_t bar_id = 1u + static_cast<uint32_t>(wg);
     const int row0 = grp * kRows;
     const int c0 = wg * kCols;
-    load_queries<kRows, k8>(p, g, row0, qs, rf_s, st, kSoftmax);
+    load_queries<kRows, k8, kSoftmax>(p, g, row0, qs, rf_s, st);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(q_bar));
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       auto scores = [&] {
         uint32_t sv[kCols];
         if (ok) {
-          tmem_ld_cols<kCols>(s_at, sv);
+          tmem_ld16(s_at, sv);
           tmem_wait_ld();
         } else {
 #pragma unroll
@@ -628,8 +628,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
         {
           const float m =
               warp_rows_reduce<kCols, true>(*reinterpret_cast<float(*)[kCols]>(e), lane);
-          if (kCols == 32 || (lane & 1) == 0)
-            red[q4 * kRows + c0 + (kCols == 32 ? lane : (lane >> 1) & 15)] = m;
+          if ((lane & 1) == 0) red[q4 * kRows + c0 + (lane >> 1)] = m;
         }
         int c_new = c_exp;
         if constexpr (k8) {
@@ -723,8 +722,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     {
       const float v =
           warp_rows_reduce<kCols, false>(*reinterpret_cast<float(*)[kCols]>(lsum), lane);
-      if (kCols == 32 || (lane & 1) == 0)
-        red[q4 * kRows + c0 + (kCols == 32 ? lane : (lane >> 1) & 15)] = v;
+      if ((lane & 1) == 0) red[q4 * kRows + c0 + (lane >> 1)] = v;
     }
     named_barrier_sync(bar_id, 128);
     const size_t part = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks + chunk;
@@ -754,7 +752,6 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     tc_fence_before();
   }
   __syncthreads();
-  grid_launch_dependents();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, static_cast<uint32_t>(Sh::kTmemCols));
@@ -776,34 +773,38 @@ struct TreeMergeParams {
 };
 
 constexpr int kMergeWarps = 8;
-constexpr int kMergeChunks = 8;  // partials a warp has in flight
+constexpr int kMergeChunks = 4;  // partials a warp has in flight
 constexpr int kMergeTokens = 4;  // new tokens a warp has in flight
 
-// One running (maximum, sum, weighted sum) of a warp, lane l owning elements
-// 4 l .. 4 l + 3; maxima in base-2 units.
+// One running (maximum, sums, weighted sum) of a warp in base-2 units: lane l
+// owns elements 4 l .. 4 l + 3 of the weighted sum; `l` is the chunks' sum, the
+// same in every lane, `lt` the new tokens' (lane l: those of slot l / 8).
 struct MergeState {
-  float m, l;
+  float m, l, lt;
   float4 o;
 };
 
-__device__ __forceinline__ void merge_in(MergeState& a, float m, float l, const float4& o,
-                                         float weight) {
-  if (m > a.m) {
-    const float s = a.m == neg_inf() ? 0.0f : exp2f(a.m - m);
-    a.o.x *= s;
-    a.o.y *= s;
-    a.o.z *= s;
-    a.o.w *= s;
-    a.l *= s;
-    a.m = m;
-  }
-  const float w = m == neg_inf() ? 0.0f : exp2f(m - a.m);
-  if (m == neg_inf()) return;
-  a.o.x = fmaf(w * weight, o.x, a.o.x);
-  a.o.y = fmaf(w * weight, o.y, a.o.y);
-  a.o.z = fmaf(w * weight, o.z, a.o.z);
-  a.o.w = fmaf(w * weight, o.w, a.o.w);
-  a.l = fmaf(w, l, a.l);
+// Raise the maximum to at least `high`; the reference to take exponents over (0
+// while nothing finite has been seen).
+__device__ __forceinline__ float merge_raise(MergeState& a, float high) {
+  const float mn = fmaxf(a.m, high);
+  const float ref = mn == neg_inf() ? 0.0f : mn;
+  const float s = exp2_fast(a.m - ref);
+  a.o.x *= s;
+  a.o.y *= s;
+  a.o.z *= s;
+  a.o.w *= s;
+  a.l *= s;
+  a.lt *= s;
+  a.m = mn;
+  return ref;
+}
+
+__device__ __forceinline__ void merge_add(MergeState& a, float w, const float4& v) {
+  a.o.x = fmaf(w, v.x, a.o.x);
+  a.o.y = fmaf(w, v.y, a.o.y);
+  a.o.z = fmaf(w, v.z, a.o.z);
+  a.o.w = fmaf(w, v.w, a.o.w);
 }
 
 // Four elements of a cached row.
@@ -832,42 +833,44 @@ __device__ __forceinline__ float4 cache_values(const uint2& raw) {
   }
 }
 
-// p.warps warps per (token, query head).  Warp w takes chunks w, w + warps, ...
-// and the visible new tokens j = w, w + warps, ... in order; the warps' states
-// are then added in order.  Bit-identical from run to run.
+// p.warps warps per (token, query head).  Warp w takes the visible new tokens
+// j = w, w + warps, ..., four at a time, and then chunks w, w + warps, ..., four
+// at a time, in order, the first chunks' loads issued before all else; the warps'
+// states are then added in order.  Bit-identical from run to run.
 template <bool k8>
-__global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const TreeMergeParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 4)
+    attn_tree_merge_kernel(const TreeMergeParams p) {
   __shared__ float4 red_o[kMergeWarps][32];
   __shared__ float red_l[kMergeWarps], red_m[kMergeWarps];
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int w = warp % p.warps;
-  const int wid = blockIdx.x * (kMergeWarps / p.warps) + warp / p.warps;
-  MergeState st{neg_inf(), 0.0f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int w = warp & (p.warps - 1);
+  const int wid = (blockIdx.x * kMergeWarps + warp) / p.warps;
+  MergeState st{neg_inf(), 0.0f, 0.0f, make_float4(0.f, 0.f, 0.f, 0.f)};
   const bool in = wid < p.T * p.nq;
   const int i = in ? wid / p.nq : 0;
-  const int h = in ? wid % p.nq : 0;
+  const int h = in ? wid - i * p.nq : 0;
   const int g = h / p.G;
   if (in) {
-    const int rr = i * p.G + h % p.G;
-    const int grp = rr / p.rows, n = rr % p.rows;
-    const size_t base = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks;
-    for (int c0 = w; c0 < p.chunks; c0 += p.warps * kMergeChunks) {
-      float2 ml[kMergeChunks];
-      float4 o[kMergeChunks];
+    const int rr = i * p.G + h - g * p.G;
+    const int grp = rr / p.rows, n = rr - grp * p.rows;
+    const size_t base = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks * p.rows + n;
+    float2 ml[kMergeChunks];
+    float4 o[kMergeChunks];
+    auto load_chunks = [&](int c0) {
 #pragma unroll
       for (int k = 0; k < kMergeChunks; ++k) {
         const int c = c0 + k * p.warps;
+        ml[k] = make_float2(neg_inf(), 0.0f);
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c < p.chunks) {
-          const size_t at = (base + c) * p.rows + n;
+          const size_t at = base + static_cast<size_t>(c) * p.rows;
           ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
           o[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kAttnHeadDim) + lane);
         }
       }
-#pragma unroll
-      for (int k = 0; k < kMergeChunks; ++k)
-        if (c0 + k * p.warps < p.chunks) merge_in(st, ml[k].x, ml[k].y, o[k], 1.0f);
-    }
+    };
+    load_chunks(w);
     // the new tokens that row i sees
     const float f = p.scale * 1.4426950408889634f;
     const float4 q = cache_values<false>(
@@ -877,9 +880,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
     const unsigned long long mine =
         (p.warps == 8 ? 0x0101010101010101ull : p.warps == 4 ? 0x1111111111111111ull
          : p.warps == 2 ? 0x5555555555555555ull : ~0ull) << w;
-    const int words = (p.T + 63) / 64;
     const size_t row0 = static_cast<size_t>(g) * p.max_len + p.past;
-    for (int word = 0; word < words; ++word) {
+    for (int word = 0; word < p.words; ++word) {
       const int left = p.T - word * 64;                       // tokens from this word on
       unsigned long long bits = left >= 64 ? ~0ull : (1ull << left) - 1ull;
       if (p.mask != nullptr) {
@@ -891,37 +893,59 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
       bits &= mine;
       while (bits != 0ull) {
         uint2 kr[kMergeTokens], vr[kMergeTokens];
-        float ks[kMergeTokens], vs[kMergeTokens], s[kMergeTokens];
+        float s[kMergeTokens], ks = 1.0f, vs = 1.0f;
+        const int slot = lane >> 3;  // the token whose score this lane will hold
         int count = 0;
 #pragma unroll
         for (int k = 0; k < kMergeTokens; ++k) {
+          kr[k] = vr[k] = make_uint2(0, 0);
           if (bits != 0ull) {
             const int j = word * 64 + __ffsll(static_cast<long long>(bits)) - 1;
             bits &= bits - 1ull;
             kr[k] = cache_raw<k8>(p.cache[0], row0 + j, lane);
             vr[k] = cache_raw<k8>(p.cache[1], row0 + j, lane);
-            ks[k] = k8 ? __ldcg(p.cache_scale[0] + row0 + j) : 1.0f;
-            vs[k] = k8 ? __ldcg(p.cache_scale[1] + row0 + j) : 1.0f;
+            if (k8 && slot == k) {
+              ks = __ldcg(p.cache_scale[0] + row0 + j);
+              vs = __ldcg(p.cache_scale[1] + row0 + j);
+            }
             count = k + 1;
           }
         }
 #pragma unroll
         for (int k = 0; k < kMergeTokens; ++k) {
-          s[k] = 0.0f;
-          if (k < count) {
-            const float4 kv = cache_values<k8>(kr[k]);
-            s[k] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, q.w * kv.w)));
-          }
+          const float4 kv = cache_values<k8>(kr[k]);
+          s[k] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, q.w * kv.w)));
         }
+        const float dot = warp_rows_reduce<kMergeTokens, false>(s, lane);
+        const float t = slot < count ? dot * ks * f : neg_inf();
+        float high = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 16));
+        const float ref = merge_raise(st, high);
+        const float e = exp2_fast(t - ref);
+        st.lt += e;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-          for (int k = 0; k < kMergeTokens; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-#pragma unroll
-        for (int k = 0; k < kMergeTokens; ++k)
-          if (k < count) merge_in(st, s[k] * ks[k] * f, 1.0f, cache_values<k8>(vr[k]), vs[k]);
+        for (int k = 0; k < kMergeTokens; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, e * vs, 8 * k);
+          if (k < count) merge_add(st, wk, cache_values<k8>(vr[k]));
+        }
       }
     }
+    for (int c0 = w; c0 < p.chunks; c0 += p.warps * kMergeChunks) {
+      if (c0 != w) load_chunks(c0);
+      float high = ml[0].x;
+#pragma unroll
+      for (int k = 1; k < kMergeChunks; ++k) high = fmaxf(high, ml[k].x);
+      const float ref = merge_raise(st, high);
+#pragma unroll
+      for (int k = 0; k < kMergeChunks; ++k) {
+        const float e = exp2_fast(ml[k].x - ref);
+        st.l = fmaf(e, ml[k].y, st.l);
+        merge_add(st, e, o[k]);
+      }
+    }
+    // the new tokens' sum over their slots
+    st.lt += __shfl_xor_sync(0xffffffffu, st.lt, 8);
+    st.l += st.lt + __shfl_xor_sync(0xffffffffu, st.lt, 16);
   }
   if (p.warps > 1) {
     red_o[warp][lane] = st.o;
@@ -933,11 +957,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const
     if (w != 0) return;
     float m = st.m;
     for (int k = 1; k < p.warps; ++k) m = fmaxf(m, red_m[warp + k]);
+    const float ref = m == neg_inf() ? 0.0f : m;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.0f;
     for (int k = 0; k < p.warps; ++k) {
-      const float mk = red_m[warp + k];
-      const float f = mk == neg_inf() ? 0.0f : exp2f(mk - m);
+      const float f = exp2_fast(red_m[warp + k] - ref);
       const float4 v = red_o[warp + k][lane];
       o.x = fmaf(f, v.x, o.x);
       o.y = fmaf(f, v.y, o.y);

@@ -1,0 +1,556 @@
+// attn_tree_wide_kernel.cuh -- attn_tree_kernel's part of the work (the cached keys
+// against the T G query rows of a key-value head) for more than 64 rows, where
+// the tensor cores and the exponentials bound it and no longer the cache.
+//
+// Query rows as M, keys as N: a thread owns a query row (a TMEM lane), so the
+// row's maximum and sum are a register each and nothing is exchanged between
+// threads.  Two warpgroups of softmax threads each work on a tile of their own,
+// with its own scores S_t, accumulator O_t (TMEM) and weights P_t (shared
+// memory), so that one's exponentials overlap the other's products:
+//   bf16, more than 128 rows ("shared"): 256 rows a block, tile t = rows
+//     [128 t, 128 t + 128); both tiles read every key block, so a key block
+//     crosses from L2 once for 256 rows
+//   else ("split"): 128 rows a block, tile t = key blocks t, t + 2, ...; each
+//     writes a partial of its own
+// Unit i of the block's work belongs to tile i % 2 and to key block i / 2
+// (shared) or i (split):
+//   S_t = Q_t K_b^T             tcgen05.mma, after unit i - 2's value product: a
+//                               tile's scores are ready only when its weights are
+//                               free again, so one wait covers both
+//   softmax                     p = 2^(t - m) straight from the scores with the
+//                               running m; only if a sum passes 2^20 (or an 8-bit
+//                               weight the range of its terms) is m raised and the
+//                               block done again
+//   O_t += P_t V_b              tcgen05.mma, V read MN-major as it lies
+// A tile waits for its own two products, and the other tile's exponentials fill
+// that time.  Issuing a unit's scores before the value product of the tile's last
+// one (scores read early, weights held in registers until P_t is free) was slower:
+// WIDE_EARLY_FIGURES
+// 8-bit caches: queries in two E4M3 parts, weights (times the value scales) in
+// three E5M2 parts, as in attn_tree_kernel; here a row's m bounds the products
+// p * scale themselves, so a key of a large value scale and a small weight costs
+// the others nothing.
+#pragma once
+
+#include <type_traits>
+
+#include "attn_tree_kernel.cuh"
+
+namespace tpb {
+
+constexpr int kWideThreads = 64 + 256;   // TMA warp, MMA warp, two softmax warpgroups
+constexpr int kWideMaxStages = 10;
+constexpr float kWideLazyLog2 = 16.0f;          // bf16: weights up to 2^16
+constexpr float kWideProductMax = 57344.0f;     // the largest E5M2 value
+constexpr float kWideProductLog2 = 5.0f;        // a raise leaves products up to 2^5
+constexpr float kWideSumMaxKv8 = 1.2676506e30f; // 2^100
+
+template <bool k8, bool kShared>
+struct WideShape {
+  static constexpr int kKItems = k8 ? 1 : 2;            // stages per K (and per V) block
+  static constexpr int kTileRows = kShared ? 256 : 128; // rows of a block
+  static constexpr int kQBytes = (kShared ? 2 : 1) * 32768;
+  static constexpr int kPBytes = k8 ? 3 * 16384 : 0;      // one tile's weights in shared memory
+  static constexpr int kScaleBytes = k8 ? 2 * 2 * 3 * 128 * 4 : 0;  // [tile][slot][3][128]
+  static constexpr int kSmallBytes = kScaleBytes + 256 * 4 + 384;
+  static constexpr int kFit =
+      (227 * 1024 - 1024 - kSmallBytes - kQBytes - 2 * kPBytes) / kTreeStageBytes;
+  static constexpr int kStages = kFit > kWideMaxStages ? kWideMaxStages : kFit;
+  static constexpr int kSmem = 1024 + kStages * kTreeStageBytes + kQBytes + 2 * kPBytes + kSmallBytes;
+  static_assert(kStages >= 2 * kKItems + 1, "K and V of a block and the next K in flight");
+};
+
+template <bool k8, bool kShared>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    attn_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                          const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
+  using Sh = WideShape<k8, kShared>;
+  constexpr int kStages = Sh::kStages;
+  constexpr int kItems = Sh::kKItems;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = smem;
+  uint8_t* qs = ring + kStages * kTreeStageBytes;
+  uint8_t* ps = qs + Sh::kQBytes;                                 // [tile]
+  float* rf_s = reinterpret_cast<float*>(ps + 2 * Sh::kPBytes);   // [256] score factors
+  float* sc_s = rf_s + 256;                                       // 8 bits: [tile][slot][3][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sc_s + Sh::kScaleBytes / 4);
+  uint64_t* full_bar = bars;                       // [kWideMaxStages]
+  uint64_t* empty_bar = full_bar + kWideMaxStages; // [kWideMaxStages]
+  uint64_t* q_bar = empty_bar + kWideMaxStages;
+  uint64_t* s_full = q_bar + 1;    // [tile] scores of a unit, P_t free, O_t up to date
+  uint64_t* p_full = s_full + 2;   // [tile] weights written, O rescaled
+  uint64_t* o_done = p_full + 2;   // [tile] the last unit's value product done
+  uint64_t* final_bar = o_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int chunk = blockIdx.x;
+  const int g = blockIdx.y;
+  const int grp = blockIdx.z;
+  const int blk0 = chunk * p.nb;
+  const int nbc = p.nblk - blk0 < p.nb ? p.nblk - blk0 : p.nb;  // at least 1
+  const int key0 = blk0 * 128;
+  const int units = kShared ? 2 * nbc : nbc;
+  // The ring's order: the first blocks' keys (`pre` of them), then the values of
+  // block x and the keys of block x + pre in turn (shared: the other way round,
+  // for tile 0 reads the next keys before tile 1 reads the values).
+  const int pre = kShared || nbc < 2 ? 1 : 2;
+  auto k_pos = [&](int x) { return x < pre ? x : 2 * x - pre + (kShared ? 0 : 1); };
+  auto v_pos = [&](int x) {
+    return kShared ? pre + (x + 1 < nbc - pre ? x + 1 : nbc - pre) + x
+                   : pre + (x < nbc - pre ? x : nbc - pre) + x;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    mbar_init(smem_u32(q_bar), 8);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&s_full[t]), 1);
+      mbar_init(smem_u32(&p_full[t]), 4);
+      mbar_init(smem_u32(&o_done[t]), 1);
+    }
+    mbar_init(smem_u32(final_bar), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // S_0, S_1 at columns 0 and 128, O_0, O_1 at 256, 384
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer
+      prefetch_tmap(&tmap_k);
+      prefetch_tmap(&tmap_v);
+      grid_dependency_wait();  // a preceding kernel may still write the cache
+      fence_proxy_async_global();
+      uint32_t issued = 0u, phases = 0u;
+      int s = 0;
+      uint32_t ph = 0u;
+      bool ok = true;
+      auto load = [&](bool is_v, int b) {
+        const int kb = key0 + b * 128;
+        for (int it = 0; it < kItems && ok; ++it) {
+          if (!wait_parity(smem_u32(&empty_bar[s]), ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(&full_bar[s]);
+          const uint32_t dst = smem_u32(ring + s * kTreeStageBytes);
+          mbar_arrive_expect_tx(fb, kTreeStageBytes);
+          if constexpr (k8) {
+            tma_load_3d(dst, is_v ? &tmap_v : &tmap_k, fb, 0, kb, g);
+          } else if (!is_v) {  // item: one 64-wide half of d, 128 keys
+            tma_load_3d(dst, &tmap_k, fb, it * 64, kb, g);
+          } else {             // item: 64 keys, both halves of d
+            tma_load_3d(dst, &tmap_v, fb, 0, kb + it * 64, g);
+            tma_load_3d(dst + kTreeStageBytes / 2, &tmap_v, fb, 64, kb + it * 64, g);
+          }
+          issued |= 1u << s;
+          phases = (phases & ~(1u << s)) | (ph << s);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      };
+      for (int x = 0; x < pre; ++x) load(false, x);
+      for (int x = 0; x < nbc && ok; ++x) {
+        if (kShared && x + pre < nbc) load(false, x + pre);
+        load(true, x);
+        if (!kShared && x + pre < nbc) load(false, x + pre);
+      }
+      if (*abort_flag) {
+        for (int st = 0; st < kStages; ++st)
+          if (issued & (1u << st))
+            drain_wait(smem_u32(&full_bar[st]), (phases >> st) & 1u, 50ull * 1000ull * 1000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- MMA issuer: units 0 and 1's scores, then unit i's values and
+      // unit i + 2's scores
+      bool ok = wait_parity(smem_u32(q_bar), 0, abort_flag);
+      tc_fence_after();
+      auto stage_of = [&](int pos, int it, uint32_t& ph) -> int {
+        const int n = pos * kItems + it;
+        ph = static_cast<uint32_t>(n / kStages) & 1u;
+        return n % kStages;
+      };
+      auto scores = [&](int i) {
+        const int t = i & 1, b = kShared ? i >> 1 : i;
+        const uint32_t d = tmem + static_cast<uint32_t>(t * 128);
+        const uint32_t q = smem_u32(qs) + (kShared ? t * 32768u : 0u);
+        for (int it = 0; it < kItems && ok; ++it) {
+          uint32_t ph;
+          const int s = stage_of(k_pos(b), it, ph);
+          ok = wait_parity(smem_u32(&full_bar[s]), ph, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
+          if constexpr (k8) {
+            constexpr uint32_t idesc = idesc_f8_f32(128, 128, false, false, false, false);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_f8(d, desc_kmajor_sw128(q + part * 16384u + kk * 32u),
+                        desc_kmajor_sw128(st + kk * 32u), idesc, part + kk > 0 ? 1u : 0u);
+          } else {
+            constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16(d, desc_kmajor_sw128(q + it * 16384u + kk * 32u),
+                        desc_kmajor_sw128(st + kk * 32u), idesc, it + kk > 0 ? 1u : 0u);
+          }
+          if (!kShared || t == 1) umma_commit(smem_u32(&empty_bar[s]));
+        }
+        if (ok) umma_commit(smem_u32(&s_full[t]));
+      };
+      auto values = [&](int i) {
+        const int t = i & 1, b = kShared ? i >> 1 : i;
+        const bool first = i < 2;
+        ok = wait_parity(smem_u32(&p_full[t]), (i >> 1) & 1, abort_flag);
+        const uint32_t d = tmem + 256u + static_cast<uint32_t>(t * 128);
+        const uint32_t pb = smem_u32(ps) + static_cast<uint32_t>(t * Sh::kPBytes);
+        for (int it = 0; it < kItems && ok; ++it) {
+          uint32_t ph;
+          const int s = stage_of(v_pos(b), it, ph);
+          ok = wait_parity(smem_u32(&full_bar[s]), ph, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
+          if constexpr (k8) {
+            constexpr uint32_t idesc = idesc_f8_f32(128, 128, true, false, false, true);
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_f8(d, desc_kmajor_sw128(pb + part * 16384u + kk * 32u),
+                        desc_mnmajor_sw128(st + kk * 4096u, 0), idesc,
+                        (!first || part + kk > 0) ? 1u : 0u);
+          } else {
+            constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, true);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16_ta(d, tmem + static_cast<uint32_t>(t * 128 + it * 32 + kk * 8),
+                           desc_mnmajor_sw128(st + kk * 2048u, kTreeStageBytes / 2), idesc,
+                           (!first || it + kk > 0) ? 1u : 0u);
+          }
+          if (!kShared || t == 1) umma_commit(smem_u32(&empty_bar[s]));
+        }
+        if (ok && i + 2 >= units) umma_commit(smem_u32(&o_done[t]));
+      };
+      for (int i = 0; i < 2 && i < units && ok; ++i) scores(i);
+      for (int i = 0; i < units && ok; ++i) {
+        values(i);
+        if (ok && i + 2 < units) scores(i + 2);
+      }
+      umma_commit(smem_u32(final_bar));
+      drain_wait(smem_u32(final_bar), 0, 50ull * 1000ull * 1000ull);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax: thread r of tile t owns its query row r.  Every
+    // thread takes the same barriers and arrivals whatever its waits returned.
+    grid_dependency_wait();  // qkv; and the partials may still be read
+    grid_launch_dependents();
+    const int st = threadIdx.x - 64;
+    const int t = st >> 7;
+    const int q4 = warp & 3;
+    const int r = q4 * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(q4 * 32) << 16;
+    const int row0 = grp * Sh::kTileRows + (kShared ? t * 128 : 0);
+    if constexpr (kShared)
+      load_queries<128, k8, 128>(p, g, row0, qs + t * 32768, rf_s + t * 128, st & 127);
+    else
+      load_queries<128, k8, 256>(p, g, row0, qs, rf_s, st);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(q_bar));
+    append_rows<k8>(p, g, chunk + p.chunks * grp, p.chunks * p.groups, st, 256);
+    named_barrier_sync(3, 256);  // rf_s is written
+    const float rf = k8 ? rf_s[(kShared ? t * 128 : 0) + r] : p.scale_log2;
+    const int mine = kShared ? nbc : (nbc - t + 1) / 2;  // this tile's units
+    auto key_of = [&](int k) { return key0 + (kShared ? k : 2 * k + t) * 128; };
+
+    float m = kUnsetMax, l = 0.0f;
+    bool ok = true;
+    float k_next = 0.0f, v_next = 0.0f;
+    const size_t sc_row = static_cast<size_t>(g) * p.max_len + r;
+    if constexpr (k8) {
+      if (mine > 0 && key_of(0) + r < p.past) {
+        k_next = __ldg(p.cache_scale[0] + sc_row + key_of(0));
+        v_next = __ldg(p.cache_scale[1] + sc_row + key_of(0));
+      }
+    }
+    const uint32_t s_at = tmem + lane_addr + static_cast<uint32_t>(t * 128);
+    const uint32_t o_at = tmem + lane_addr + 256u + static_cast<uint32_t>(t * 128);
+    uint8_t* pt = ps + t * Sh::kPBytes + r * 128;
+    const int sw = r & 7;
+    for (int k = 0; k < mine; ++k) {
+      const int left = p.past - key_of(k);  // keys from this block on
+      const float* ks = nullptr;            // this block's key scales, value scales, log2 of them
+      if constexpr (k8) {
+        float* slot = sc_s + (t * 2 + (k & 1)) * 3 * 128;
+        slot[r] = k_next;
+        slot[128 + r] = v_next;
+        slot[256 + r] = __log2f(v_next);
+        ks = slot;
+        k_next = v_next = 0.0f;
+        if (k + 1 < mine && key_of(k + 1) + r < p.past) {
+          k_next = __ldg(p.cache_scale[0] + sc_row + key_of(k + 1));
+          v_next = __ldg(p.cache_scale[1] + sc_row + key_of(k + 1));
+        }
+        named_barrier_sync(1u + static_cast<uint32_t>(t), 128);
+      }
+      ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&s_full[t]), k & 1, abort_flag));
+      tc_fence_after();
+      // 32 raw scores from column c on
+      auto fetch = [&](int c, uint32_t (&sv)[32]) {
+        if (ok) {
+          tmem_ld32(s_at + static_cast<uint32_t>(c), sv);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sv[j] = 0u;
+        }
+      };
+      // ... in base-2 units less `base`; behind the cache's last key: -inf
+      auto scaled = [&](const uint32_t (&sv)[32], int c, float base, bool tail, float2 (&e)[16]) {
+        const float2 f = make_float2(rf, rf), nb = make_float2(-base, -base);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 s = make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
+          if constexpr (k8)
+            e[j] = fma2(s, mul2(f, *reinterpret_cast<const float2*>(ks + c + 2 * j)), nb);
+          else
+            e[j] = fma2(s, f, nb);
+        }
+        if (tail) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (c + 2 * j >= left) e[j].x = neg_inf();
+            if (c + 2 * j + 1 >= left) e[j].y = neg_inf();
+          }
+        }
+      };
+      // the block's weights with the running m into P_t; their sum, and (8 bits) the
+      // largest product with a value scale
+      float2 acc = make_float2(0.0f, 0.0f);
+      float top = 0.0f;
+      auto weights32 = [&](const uint32_t (&sv)[32], int c, bool tail) {
+        float2 e[16];
+        scaled(sv, c, m, tail, e);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          e[j] = make_float2(exp2_fast(e[j].x), exp2_fast(e[j].y));
+          acc = add2(acc, e[j]);
+          if constexpr (k8) {
+            e[j] = mul2(e[j], *reinterpret_cast<const float2*>(ks + 128 + c + 2 * j));
+            top = fmaxf(top, fmaxf(e[j].x, e[j].y));
+          }
+        }
+        // bf16: over the scores, two keys a column (this lane's columns below c + 32
+        // have been read).  8 bits: three parts of 128-byte rows, 16-byte piece j at
+        // j ^ (r % 8)
+        if constexpr (k8) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 a4, b4, c4;
+            split_weights(e + 8 * h, a4, b4, c4);
+            uint8_t* at = pt + (((c / 16 + h) ^ sw) << 4);
+            *reinterpret_cast<uint4*>(at) = a4;
+            *reinterpret_cast<uint4*>(at + 16384) = b4;
+            *reinterpret_cast<uint4*>(at + 32768) = c4;
+          }
+        } else {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(e[j].x, e[j].y);
+          tmem_st16(s_at + static_cast<uint32_t>(c / 2), pk);
+        }
+      };
+      auto weights = [&](auto tail) {
+        uint32_t sa[32], sb[32];
+        acc = make_float2(0.0f, 0.0f);
+        top = 0.0f;
+        fetch(0, sa);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {  // the next scores on their way meanwhile
+          tmem_wait_ld();
+          fetch(c + 32, sb);
+          weights32(sa, c, tail);
+          tmem_wait_ld();
+          if (c == 0) fetch(64, sa);
+          weights32(sb, c + 32, tail);
+        }
+      };
+      // raise m by the block's maximum where `need`; l and O follow
+      auto raise = [&](bool need, float high, float product) {
+        // 8 bits: products up to 2^5, and no weight above 2^60
+        float mn = k8 ? fmaxf(product - kWideProductLog2, high - 60.0f) : high;
+        mn = need ? fmaxf(m, mn) : m;
+        // in two steps: an 8-bit row's m may rise by more than fp32's exponents
+        const float half = exp2f(0.5f * (m - mn));
+        l = l * half * half;
+        m = mn;
+        if (k > 0 && ok) {  // O holds the products of the tile's earlier units
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_at + static_cast<uint32_t>(c), o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              o[j] = __float_as_uint(__uint_as_float(o[j]) * half * half);
+            tmem_st16(o_at + static_cast<uint32_t>(c), o);
+          }
+          tmem_wait_st();
+        }
+      };
+      auto all_weights = [&] {
+        if (left < 128)
+          weights(std::true_type{});
+        else
+          weights(std::false_type{});
+      };
+      if constexpr (!k8) {
+        // the maximum first: the weights go over the scores.  m stays while no
+        // weight passes 2^kWideLazyLog2
+        float high = kUnsetMax;
+        uint32_t sa[32], sb[32];
+        fetch(0, sa);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          tmem_wait_ld();
+          fetch(c + 32, sb);
+          if (left < 128) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j >= left) sa[j] = 0xff800000u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(sa[j]));
+          tmem_wait_ld();
+          if (c == 0) fetch(64, sa);
+          if (left < 128) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + 32 + j >= left) sb[j] = 0xff800000u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(sb[j]));
+        }
+        high *= rf;
+        const bool need = high - m > kWideLazyLog2;
+        if (__any_sync(0xffffffffu, need)) raise(need, high, 0.0f);
+        all_weights();
+      } else {
+        bool need = k == 0, raised = false;
+        for (;;) {
+          if (__any_sync(0xffffffffu, need)) {
+            raised = true;
+            float high = kUnsetMax, product = kUnsetMax;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t sv[32];
+              float2 e[16];
+              fetch(c, sv);
+              tmem_wait_ld();
+              scaled(sv, c, 0.0f, left < 128, e);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                high = fmaxf(high, fmaxf(e[j].x, e[j].y));
+                const float2 lv = *reinterpret_cast<const float2*>(ks + 256 + c + 2 * j);
+                product = fmaxf(product, fmaxf(e[j].x + lv.x, e[j].y + lv.y));
+              }
+            }
+            raise(need, high, product);
+          }
+          all_weights();
+          // (NaN raises once, for nothing)
+          need = !(top <= kWideProductMax) || !(acc.x + acc.y <= kWideSumMaxKv8);
+          if (raised || !__any_sync(0xffffffffu, need)) break;
+        }
+      }
+      l += acc.x + acc.y;
+      if constexpr (k8)
+        fence_proxy_async_smem();  // the weights are read by the MMA through the async proxy
+      else
+        tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
+    }
+    // both tiles': the ring is used again below
+    for (int x = 0; x < 2 && x < units; ++x)
+      ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[x]), 0, abort_flag));
+    tc_fence_after();
+    // the partial, with the sum brought to [1, 2): m then stands for the row's
+    // mass whatever the value scales were
+    const int le = static_cast<int>((__float_as_uint(l) >> 23) & 0xFFu) - 127;
+    const int shift = l > 0.0f && le > -127 && le < 128 ? (le < -126 ? -126 : le > 126 ? 126 : le) : 0;
+    const float down = pow2i(-shift);
+    const size_t part = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks * (kShared ? 1 : 2) +
+                        (kShared ? chunk : 2 * chunk + t);
+    const size_t out_row = part * Sh::kTileRows + (kShared ? t * 128 : 0) + r;
+    const bool in = row0 + r < p.R;
+    if (in)
+      *reinterpret_cast<float2*>(p.part_ml + out_row * 2) =
+          make_float2(m + static_cast<float>(shift), l * down);
+    // O row by row: a warp turns 64 columns of its 32 rows at a time through 8 KB
+    // of P_t, or of the ring, which is empty by now (16-byte piece c of row r at c ^ (r % 16)), so that 16 lanes
+    // write 256 contiguous bytes
+    uint8_t* turn = (k8 ? ps + t * Sh::kPBytes : ring + t * 32768) + q4 * 8192;
+    float4* po = reinterpret_cast<float4*>(p.part_o + (out_row - lane) * kAttnHeadDim);
+    const bool have = ok && mine > 0;  // unwritten TMEM may hold anything
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 16) {
+        uint32_t o[16];
+        if (have) {
+          tmem_ld16(o_at + static_cast<uint32_t>(half * 64 + c), o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float4*>(turn + lane * 256 + (((c / 4 + j) ^ (lane & 15)) << 4)) =
+              have ? make_float4(__uint_as_float(o[4 * j]) * down,
+                                 __uint_as_float(o[4 * j + 1]) * down,
+                                 __uint_as_float(o[4 * j + 2]) * down,
+                                 __uint_as_float(o[4 * j + 3]) * down)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      __syncwarp();
+#pragma unroll 4
+      for (int i = 0; i < 32; i += 2) {
+        const int rl = i + (lane >> 4), piece = lane & 15;
+        const float4 v = *reinterpret_cast<const float4*>(turn + rl * 256 + ((piece ^ (rl & 15)) << 4));
+        if (row0 + q4 * 32 + rl < p.R) po[rl * (kAttnHeadDim / 4) + half * 16 + piece] = v;
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace tpb

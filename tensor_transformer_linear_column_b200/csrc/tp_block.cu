@@ -16,6 +16,7 @@
 #include "attn_kernel.cuh"
 #include "attn_prefill_kernel.cuh"
 #include "attn_tree_kernel.cuh"
+#include "attn_tree_wide_kernel.cuh"
 #include "colsum_kernel.cuh"
 #include "diag_kernel.cuh"
 #include "kv_cache_kernel.cuh"
@@ -109,28 +110,51 @@ PairKernel pair_kernel_for(int epi, bool a_mn, bool b_mn) {
   return nullptr;
 }
 
-// The tree-attention kernel's instantiations by query rows per block (16, 32,
-// 64, 128), for a bf16 and for an 8-bit cache.
+// The tree-attention kernels' instantiations for a bf16 and for an 8-bit cache:
+// 16, 32 or 64 query rows per block, then the wide kernel's 128 rows (the key
+// blocks split between its two tiles) and, bf16, 256 (shared by them).
 using TreeKernel = void (*)(const CUtensorMap, const CUtensorMap, const tpb::TreeParams);
 struct TreeLaunch {
   TreeKernel kernel;
   int rows, threads, smem, blocks_per_sm;
+  int partials;  // per chunk
 };
 template <int kRows, bool k8>
 constexpr TreeLaunch tree_launch() {
   using Sh = tpb::TreeShape<kRows, k8>;
   return TreeLaunch{tpb::attn_tree_kernel<kRows, k8>, kRows, Sh::kThreads, Sh::kSmem,
-                    Sh::kBlocksPerSm};
+                    Sh::kBlocksPerSm, 1};
 }
+template <bool k8, bool kShared>
+constexpr TreeLaunch wide_launch() {
+  using Sh = tpb::WideShape<k8, kShared>;
+  return TreeLaunch{tpb::attn_tree_wide_kernel<k8, kShared>, Sh::kTileRows, tpb::kWideThreads,
+                    Sh::kSmem, 1, kShared ? 1 : 2};
+}
+const TreeLaunch kTreeLaunches[] = {
+    tree_launch<16, false>(), tree_launch<32, false>(), tree_launch<64, false>(),
+    wide_launch<false, false>(), wide_launch<false, true>()};
+const TreeLaunch kTreeLaunchesKv8[] = {tree_launch<16, true>(), tree_launch<32, true>(),
+                                       tree_launch<64, true>(), wide_launch<true, false>()};
+
+// The instantiation for `rows` query rows per key-value head: the smallest that
+// holds them, so that the cache is read once; the largest above that.
+const TreeLaunch& tree_launch_for(int rows, bool k8) {
+  if (rows <= 64) return (k8 ? kTreeLaunchesKv8 : kTreeLaunches)[rows <= 16 ? 0 : rows <= 32 ? 1 : 2];
+  if (k8) return kTreeLaunchesKv8[3];
+  return kTreeLaunches[rows <= 128 ? 3 : 4];
+}
+
+bool tree_attrs(const TreeLaunch& l) {
+  return cuda_ok(cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, l.smem),
+                 "cudaFuncSetAttribute") &&
+         cuda_ok(cudaFuncSetAttribute(l.kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      cudaSharedmemCarveoutMaxShared),
+                 "cudaFuncSetAttribute");
+}
+
 using QkKernel = void (*)(const tpb::QkParams);
 QkKernel qk_kernel(int lanes, int layout, bool backward);
-
-const TreeLaunch kTreeLaunches[2][4] = {
-    {tree_launch<16, false>(), tree_launch<32, false>(), tree_launch<64, false>(),
-     tree_launch<128, false>()},
-    {tree_launch<16, true>(), tree_launch<32, true>(), tree_launch<64, true>(),
-     tree_launch<128, true>()},
-};
 
 const DeviceInfo* device_info() {
   int dev = 0;
@@ -185,15 +209,10 @@ const DeviceInfo* device_info() {
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                "cudaFuncSetAttribute"))
     return nullptr;
-  for (const auto& kind : kTreeLaunches)
-    for (const TreeLaunch& l : kind)
-      if (!cuda_ok(cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        l.smem),
-                   "cudaFuncSetAttribute") ||
-          !cuda_ok(cudaFuncSetAttribute(l.kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                        cudaSharedmemCarveoutMaxShared),
-                   "cudaFuncSetAttribute"))
-        return nullptr;
+  for (const TreeLaunch& l : kTreeLaunches)
+    if (!tree_attrs(l)) return nullptr;
+  for (const TreeLaunch& l : kTreeLaunchesKv8)
+    if (!tree_attrs(l)) return nullptr;
   for (int lanes = 2; lanes <= 32; lanes *= 2)
     for (int variant = 0; variant < 4; ++variant) {
       QkKernel k = qk_kernel(lanes, variant & 1 ? TP_ROPE_PAIRS : TP_ROPE_HALF, (variant & 2) != 0);
@@ -845,7 +864,8 @@ tp_status check_append(const tp_bf16* qkv, const int* rows, const void* k, const
 template <bool k8>
 tp_status launch_append(const tpb::KvAppendParams& p, cudaStream_t stream) {
   const int per_block = tpb::kCacheThreads / p.lanes;
-  const int blocks = (p.n + per_block - 1) / per_block;
+  const int rows = per_block * tpb::kAppendBatch;
+  const int blocks = p.n / rows + (p.n % rows != 0 ? 1 : 0);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = launch_config(
       dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(2 * p.nkv), 1), tpb::kCacheThreads,
@@ -860,11 +880,9 @@ tp_status launch_append(const tpb::KvAppendParams& p, cudaStream_t stream) {
 
 constexpr int kTreeSms = 148;  // the plan is a function of the sizes only, as plan_attn's
 
-// Query rows per block: the smallest of 16, 32, 64 and 128 that holds the T G
-// rows of a head, so that the cache is read once; row groups of 128 above
-// that.  Chunks per head: the fewest key blocks on the busiest SM, counting
-// three for a block's set-up and partial.
-tp_status plan_tree(int T, int past, int nq, int nkv, tpb::TreeParams& p, int& which,
+// Chunks per head: the fewest key blocks on the busiest SM, counting three for a
+// block's set-up and partial.
+tp_status plan_tree(int T, int past, int nq, int nkv, bool k8, tpb::TreeParams& p,
                     size_t& part_o_bytes, size_t& part_ml_bytes) {
   p = tpb::TreeParams{};
   p.T = T;
@@ -874,8 +892,8 @@ tp_status plan_tree(int T, int past, int nq, int nkv, tpb::TreeParams& p, int& w
   p.G = nq / nkv;
   if (T > tpb::kTreeMaxTokens || p.G > 16) return TP_ERR_UNSUPPORTED;
   p.R = T * p.G;
-  which = p.R <= 16 ? 0 : p.R <= 32 ? 1 : p.R <= 64 ? 2 : 3;
-  const TreeLaunch& l = kTreeLaunches[0][which];
+  p.g_magic = 0xFFFFFFFFu / static_cast<unsigned>(p.G) + 1u;
+  const TreeLaunch& l = tree_launch_for(p.R, k8);
   p.groups = (p.R + l.rows - 1) / l.rows;
   p.nblk = past / 128 + (past % 128 != 0 ? 1 : 0);
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(tpb::kAttnHeadDim));
@@ -888,6 +906,7 @@ tp_status plan_tree(int T, int past, int nq, int nkv, tpb::TreeParams& p, int& w
       const int nb = (p.nblk + c - 1) / c;
       const int chunks = (p.nblk + nb - 1) / nb;
       const long long waves = (per_chunk * chunks + slots - 1) / slots;
+      if (waves > 4 && best != 0) break;  // more chunks only add partials
       const long long cost = waves * (nb + 3);
       if (best == 0 || cost < best) {
         best = cost;
@@ -896,7 +915,7 @@ tp_status plan_tree(int T, int past, int nq, int nkv, tpb::TreeParams& p, int& w
       }
     }
   }
-  const size_t rows = static_cast<size_t>(p.groups) * nkv * p.chunks * l.rows;
+  const size_t rows = static_cast<size_t>(p.groups) * nkv * p.chunks * l.partials * l.rows;
   part_o_bytes = rows * tpb::kAttnHeadDim * 4;
   part_ml_bytes = (rows * 2 * 4 + 255) / 256 * 256;
   return TP_OK;
@@ -919,9 +938,8 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
   if (d != tpb::kAttnHeadDim) return TP_ERR_UNSUPPORTED;
   if (t < 1 || nq % t != 0 || nkv % t != 0) return TP_ERR_TP_DEGREE;
   tpb::TreeParams p;
-  int which = 0;
   size_t po = 0, pml = 0;
-  const tp_status planned = plan_tree(T, past, nq, nkv, p, which, po, pml);
+  const tp_status planned = plan_tree(T, past, nq, nkv, k8, p, po, pml);
   if (planned != TP_OK) return planned;
   if (po + pml > 0) {
     if (workspace == nullptr || workspace_bytes < po + pml) return TP_ERR_WORKSPACE;
@@ -929,7 +947,7 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
   }
   const DeviceInfo* dev = device_info();
   if (dev == nullptr) return TP_ERR_CUDA;
-  const TreeLaunch& l = kTreeLaunches[k8 ? 1 : 0][which];
+  const TreeLaunch& l = tree_launch_for(p.R, k8);
   if (l.smem > dev->max_smem) return TP_ERR_UNSUPPORTED;
   p.max_len = max_len;
   p.qkv = qkv;
@@ -985,7 +1003,7 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
   m.nkv = nkv;
   m.G = p.G;
   m.rows = l.rows;
-  m.chunks = p.chunks;
+  m.chunks = p.chunks * l.partials;
   m.max_len = max_len;
   m.words = (T + 63) / 64;
   m.scale = 1.0f / sqrtf(static_cast<float>(d));
@@ -998,9 +1016,12 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
   m.part_o = p.part_o;
   m.part_ml = p.part_ml;
   m.ctx = ctx;
-  // about four partials or tokens per warp
-  const int items = p.chunks + (mask != nullptr ? (T < 8 ? T : 8) : (T + 1) / 2);
-  m.warps = items <= 4 ? 1 : items <= 8 ? 2 : items <= 16 ? 4 : 8;
+  // up to eight warps a row while that fills the GPU: with many rows their
+  // joining costs more than it saves
+  const int rows = T * nq;
+  const int items = m.chunks + (mask != nullptr ? (T < 8 ? T : 8) : (T + 1) / 2);
+  m.warps = rows <= 592 ? 8 : rows <= 1184 ? 4 : rows <= 2368 ? 2 : 1;
+  while (m.warps > 1 && items <= 2 * m.warps) m.warps /= 2;
   const int per_block = tpb::kMergeWarps / m.warps;
   cudaLaunchConfig_t cfg =
       launch_config(dim3(static_cast<unsigned>((T * nq + per_block - 1) / per_block), 1, 1),
@@ -1547,11 +1568,14 @@ tp_status tp_tree_mask(const int32_t* parents, int T, uint64_t* mask) {
 
 size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads, int head_dim) {
   if (!heads_ok(T, past, n_q_heads, n_kv_heads) || head_dim != tpb::kAttnHeadDim) return 0;
-  tpb::TreeParams p;
-  int which = 0;
-  size_t po = 0, pml = 0;
-  if (plan_tree(T, past, n_q_heads, n_kv_heads, p, which, po, pml) != TP_OK) return 0;
-  return po + pml;
+  size_t most = 0;
+  for (const bool k8 : {false, true}) {
+    tpb::TreeParams p;
+    size_t po = 0, pml = 0;
+    if (plan_tree(T, past, n_q_heads, n_kv_heads, k8, p, po, pml) != TP_OK) return 0;
+    most = po + pml > most ? po + pml : most;
+  }
+  return most;
 }
 
 tp_status tp_attn_tree(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,
