@@ -24,6 +24,10 @@
 // TMA in the order K_0, K_1, V_0, K_2, V_1, ...):
 //   S_b^T[key, n] = K_b Q^T       tcgen05.mma, keys as M (a TMEM lane is a key),
 //                                 query rows as N, into one of two TMEM slots
+//                                 (8 bits: the parts of an operand lie side by side
+//                                 along N and their products in columns of their own,
+//                                 so their number costs no instructions: one thread
+//                                 issues an MMA every 100 cycles whatever its N)
 //   softmax                       one key per thread: its scores against the
 //                                 running maximum m_n of each row; weights
 //                                 p = 2^(s - m) into one of two shared slots
@@ -95,7 +99,12 @@ struct TreeShape {
   static constexpr int kPartBytes = 128 * kRows * (k8 ? 1 : 2);
   static constexpr int kSlotBytes = kParts * kPartBytes;
   static constexpr int kQBytes = 2 * kRows * 128;          // hi, lo; or the two d halves
-  static constexpr int kTmemCols = kRows == 16 ? 64 : kRows == 32 ? 128 : 256;
+  static constexpr int kScoreParts = k8 ? 2 : 1;  // hi | lo along N: summed by the softmax
+  static constexpr int kOCol = 2 * kScoreParts * kRows;  // TMEM: two score slots, then O's parts
+  static constexpr int kTmemUsed = kOCol + kParts * kRows;
+  static constexpr int kTmemCols =
+      kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kTmemUsed <= 512 && kBlocksPerSm * kTmemCols <= 512, "TMEM of the blocks of an SM");
   static constexpr int kSmallBytes = (4 * kRows + 4 * kRows) * 4 + 64 + 256;
   static constexpr int kSmemTarget = kBlocksPerSm == 2 ? (228 * 1024) / 2 - 1024 : 227 * 1024;
   static constexpr int kFit = (kSmemTarget - 1024 - kSmallBytes - kQBytes - 2 * kSlotBytes) /
@@ -106,17 +115,12 @@ struct TreeShape {
   static_assert(kStages >= 4, "K, K, V and the next K in flight");
 };
 
-// Descriptor of an MN-major operand without swizzling: 16-byte vectors along MN,
-// 8 consecutive K indices 16 bytes apart (a 128-byte core matrix), core matrices
-// along K `lbo` bytes and along MN `sbo` bytes apart.
-__device__ __forceinline__ uint64_t desc_mnmajor_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  return d;
-}
+// Operand layouts in shared memory, as descriptor words:
+//   K-major or MN-major with 128-byte swizzling (desc_kmajor_sw128,
+//     desc_mnmajor_sw128): lower word desc_lo(address, LBO), upper kDescHiSw128
+//   MN-major without swizzling: 16-byte vectors along MN, 8 consecutive K indices 16
+//     bytes apart (a 128-byte core matrix), core matrices along K LBO = 128 and along
+//     MN SBO = 2048 bytes apart: lower word desc_lo(address, 128), upper kDescHiPlain
 
 // Instruction descriptor, kind::f8f6f4: fp32 D; A and B are E4M3 or E5M2.
 __host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool a_e5m2, bool b_e5m2,
@@ -126,14 +130,57 @@ __host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, bool a_e5m2, b
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 8-bit operands, one M x N x 32 step.
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// The MMAs of these kernels take a descriptor as its two words: the upper one does
+// not change, and a step along K adds to the lower one.  The warp that issues them
+// runs converged, so the words are uniform, and one elected lane issues.
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescHiPlain = (2048u >> 4) | (1u << 14);  // SBO 2048
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return (saddr >> 4) | ((lbo >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, one M x N x 16 (bf16) or x 32 (8 bits) step.
+template <bool k8>
+__device__ __forceinline__ void umma_words(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                           uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                           bool accumulate) {
+  if constexpr (k8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc),
+        "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc),
+        "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+// The bf16 step with A in tensor memory (umma_bf16_ta's layout).
+__device__ __forceinline__ void umma_words_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                              uint32_t b_hi, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
       : "memory");
 }
 
@@ -183,71 +230,72 @@ __device__ __forceinline__ uint32_t half2_of_e4m3x2(uint32_t codes) {
 // Query rows [row0, row0 + kRows) of head g into shared memory as a K-major
 // operand, by kThreads threads (16 lanes a row): bf16 as two 64-wide halves, or
 // the 8-bit hi / lo parts with each row's factor in rf_s.  Rows at or past R are
-// zero.  Up to four rows a thread in flight and rolled beyond that: a block runs
-// this once, and each instruction line it has to fetch costs more than the loop
-// (128 rows unrolled: 10,000 cycles, 16,000 in 8 bits).
+// zero.  The first call starts the copies (16 bytes a thread each; 8 bits: raw,
+// into `stage`), the second waits for this thread's and splits them.  The ring's
+// loads start after the first call: behind them these few KB would land 6,000
+// cycles later.  Rolled loops: a block runs them once, and each instruction line it
+// has to fetch costs more than the loop.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+
 template <int kRows, bool k8, int kThreads>
-__device__ __forceinline__ void load_queries(const TreeParams& p, int g, int row0, uint8_t* qs,
-                                             float* rf_s, int st) {
+__device__ __forceinline__ void start_queries(const TreeParams& p, int g, int row0, uint8_t* qs,
+                                              uint8_t* stage, int st) {
   const int l = st & 15;
-  constexpr int kPasses = kRows * 16 / kThreads;
-  constexpr int kFlight = kPasses < 4 ? kPasses : 4;
 #pragma unroll 1
-  for (int i0 = 0; i0 < kPasses; i0 += kFlight) {
-    uint4 all[kFlight];
+  for (int r = st >> 4; r < kRows; r += kThreads >> 4) {
+    const bool in = row0 + r < p.R;
+    const int rr = in ? row0 + r : 0;
+    const int tok = p.G == 1 ? rr : static_cast<int>(__umulhi(static_cast<unsigned>(rr), p.g_magic));
+    const uint16_t* src =
+        p.qkv +
+        (static_cast<size_t>(tok) * (p.nq + 2 * p.nkv) + g * p.G + rr - tok * p.G) * kAttnHeadDim +
+        8 * l;
+    // bf16: half l / 8, 16-byte chunk l % 8 of the 128-byte row, swizzled
+    uint8_t* dst = k8 ? stage + r * 256 + l * 16
+                      : qs + (l >> 3) * (kRows * 128) + r * 128 + (((l & 7) ^ (r & 7)) << 4);
+    cp_async16(smem_u32(dst), src, in);
+  }
+}
+
+template <int kRows, bool k8, int kThreads>
+__device__ __forceinline__ void finish_queries(const TreeParams& p, uint8_t* qs,
+                                               const uint8_t* stage, float* rf_s, int st) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (k8) {
+    const int l = st & 15;
+#pragma unroll 1
+    for (int r = st >> 4; r < kRows; r += kThreads >> 4) {
+      float x[8];
+      unpack8(*reinterpret_cast<const uint4*>(stage + r * 256 + l * 16), x);
+      float amax = abs_max8(x);
 #pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int rr = row0 + (st >> 4) + (i0 + i) * (kThreads >> 4);
-      all[i] = make_uint4(0, 0, 0, 0);
-      if (rr < p.R) {
-        const int tok =
-            p.G == 1 ? rr : static_cast<int>(__umulhi(static_cast<unsigned>(rr), p.g_magic));
-        const int h = g * p.G + rr - tok * p.G;
-        all[i] = __ldg(reinterpret_cast<const uint4*>(
-                           p.qkv +
-                           (static_cast<size_t>(tok) * (p.nq + 2 * p.nkv) + h) * kAttnHeadDim) +
-                       l);
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      // shift: amax 2^shift in (224, 448]
+      const uint32_t bits = __float_as_uint(amax);
+      int shift = 8 - (static_cast<int>(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+      shift = amax > 0.0f ? (shift > 126 ? 126 : shift) : 0;
+      const float up = pow2i(shift);  // at least -120
+      // in fp16 the scaled elements are exact down to 2^-14, as hi and the rest
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 v = __floats2half2_rn(x[2 * k] * up, x[2 * k + 1] * up);
+        hi[k] = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&v));
+        const uint32_t back = half2_of_e4m3x2(hi[k]);
+        const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
+        lo[k] = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&rest));
       }
-    }
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int r = (st >> 4) + (i0 + i) * (kThreads >> 4);
-      const uint4 raw = all[i];
-      if constexpr (!k8) {
-        // half l / 8, 16-byte chunk l % 8 of the 128-byte row, swizzled
-        *reinterpret_cast<uint4*>(qs + (l >> 3) * (kRows * 128) + r * 128 +
-                                  (((l & 7) ^ (r & 7)) << 4)) = raw;
-      } else {
-        float x[8];
-        unpack8(raw, x);
-        float amax = abs_max8(x);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // shift: amax 2^shift in (224, 448]
-        const uint32_t bits = __float_as_uint(amax);
-        int shift =
-            8 - (static_cast<int>(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-        shift = amax > 0.0f ? (shift > 126 ? 126 : shift) : 0;
-        const float up = pow2i(shift);  // at least -120
-        // in fp16 the scaled elements are exact down to 2^-14, as hi and the rest
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __half2 v = __floats2half2_rn(x[2 * k] * up, x[2 * k + 1] * up);
-          hi[k] = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&v));
-          const uint32_t back = half2_of_e4m3x2(hi[k]);
-          const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
-          lo[k] = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&rest));
-        }
-        const int off = r * 128 + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8;
-        *reinterpret_cast<uint2*>(qs + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-        *reinterpret_cast<uint2*>(qs + kRows * 128 + off) =
-            make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-        // a row that holds an infinity scores NaN (its parts are clamped)
-        if (l == 0)
-          rf_s[r] = amax > 3.3895314e38f ? __int_as_float(0x7fc00000)
-                                         : p.scale_log2 * pow2i(-shift);
-      }
+      const int off = r * 128 + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8;
+      *reinterpret_cast<uint2*>(qs + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+      *reinterpret_cast<uint2*>(qs + kRows * 128 + off) =
+          make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+      // a row that holds an infinity scores NaN (its parts are clamped)
+      if (l == 0)
+        rf_s[r] = amax > 3.3895314e38f ? __int_as_float(0x7fc00000) : p.scale_log2 * pow2i(-shift);
     }
   }
 }
@@ -343,7 +391,8 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
   uint64_t* full_bar = bars;                      // [kStages]
   uint64_t* empty_bar = full_bar + kTreeMaxStages;
   uint64_t* q_bar = empty_bar + kTreeMaxStages;   // the query operand is written
-  uint64_t* s_full = q_bar + 1;                   // [2] scores of a block in their slot
+  uint64_t* q_sent = q_bar + 1;                   // its copies have been started
+  uint64_t* s_full = q_sent + 1;                  // [2] scores of a block in their slot
   uint64_t* s_free = s_full + 2;                  // [2] slot read
   uint64_t* p_full = s_free + 2;                  // [2] weights written, O rescaled
   uint64_t* o_done = p_full + 2;                  // [2] the block's value product done
@@ -366,6 +415,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     mbar_init(smem_u32(q_bar), kSoftmax / 32);
+    mbar_init(smem_u32(q_sent), kSoftmax / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_free[i]), kSoftmax / 32);
@@ -384,7 +434,8 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t o_col = 2u * kRows;  // score slots at columns 0 and kRows, then O
+  constexpr uint32_t o_col = Sh::kOCol;
+  constexpr int kSlotCols = Sh::kScoreParts * kRows;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -396,7 +447,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       uint32_t issued = 0u, phases = 0u;
       int s = 0;
       uint32_t ph = 0u;
-      bool ok = true;
+      bool ok = wait_parity(smem_u32(q_sent), 0, abort_flag);
       auto load = [&](bool is_v, int b) {
         const int kb = key0 + b * 128;
         for (int it = 0; it < kItems && ok; ++it) {
@@ -435,89 +486,80 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer, in the producer's order
-      bool ok = wait_parity(smem_u32(q_bar), 0, abort_flag);
+    // ---------------- MMA issuer, in the producer's order
+    const bool elected = elect_one();
+    bool ok = __all_sync(0xffffffffu, wait_parity(smem_u32(q_bar), 0, abort_flag));
+    tc_fence_after();
+    int s = 0;
+    uint32_t ph = 0u;
+    const uint32_t q_lo = desc_lo(smem_u32(qs), 16);
+    // the next stage's tile, once it has landed
+    auto next = [&]() -> uint32_t {
+      ok = ok && __all_sync(0xffffffffu, wait_parity(smem_u32(&full_bar[s]), ph, abort_flag));
       tc_fence_after();
-      int s = 0;
-      uint32_t ph = 0u;
-      auto advance = [&] {
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
-        }
-      };
-      for (int b = 0; b <= nbc && ok; ++b) {
-        if (b < nbc) {
-          const int slot = b & 1;
-          if (b >= 2) ok = wait_parity(smem_u32(&s_free[slot]), ((b - 2) >> 1) & 1, abort_flag);
-          const uint32_t d = tmem + static_cast<uint32_t>(slot * kRows);
-          for (int it = 0; it < kItems && ok; ++it) {
-            ok = wait_parity(smem_u32(&full_bar[s]), ph, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
-            if constexpr (k8) {
-              constexpr uint32_t idesc = idesc_f8_f32(128, kRows, false, false, false, false);
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  umma_f8(d, desc_kmajor_sw128(st + kk * 32u),
-                          desc_kmajor_sw128(smem_u32(qs) + part * (kRows * 128u) + kk * 32u), idesc,
-                          part + kk > 0 ? 1u : 0u);
-            } else {
-              constexpr uint32_t idesc = idesc_bf16_f32(128, kRows);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(d, desc_kmajor_sw128(st + kk * 32u),
-                          desc_kmajor_sw128(smem_u32(qs) + it * (kRows * 128u) + kk * 32u), idesc,
-                          it + kk > 0 ? 1u : 0u);
-            }
-            umma_commit(smem_u32(&empty_bar[s]));
-            advance();
-          }
-          if (!ok) break;
-          umma_commit(smem_u32(&s_full[slot]));
-        }
-        if (b > 0) {
-          const int v = b - 1, slot = v & 1;
-          ok = wait_parity(smem_u32(&p_full[slot]), (v >> 1) & 1, abort_flag);
-          const uint32_t pb = smem_u32(ps) + static_cast<uint32_t>(slot * Sh::kSlotBytes);
-          for (int it = 0; it < kItems && ok; ++it) {
-            ok = wait_parity(smem_u32(&full_bar[s]), ph, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
-            if constexpr (k8) {
-              // 32 keys a step: V 4096 bytes on, the weights 4 core matrices on
-              constexpr uint32_t idesc = idesc_f8_f32(128, kRows, false, true, true, true);
-#pragma unroll
-              for (int part = 0; part < 3; ++part)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  umma_f8(tmem + o_col, desc_mnmajor_sw128(st + kk * 4096u, 0),
-                          desc_mnmajor_plain(pb + part * static_cast<uint32_t>(Sh::kPartBytes) +
-                                                 kk * 512u, 128, 2048),
-                          idesc, (v > 0 || part + kk > 0) ? 1u : 0u);
-            } else {
-              // 16 keys a step: V 2048 bytes on (its d halves 8 KB apart), the
-              // weights 2 core matrices on
-              constexpr uint32_t idesc = idesc_bf16_f32(128, kRows, true, true);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(tmem + o_col,
-                          desc_mnmajor_sw128(st + kk * 2048u, kTreeStageBytes / 2),
-                          desc_mnmajor_plain(pb + (it * 4 + kk) * 256u, 128, 2048), idesc,
-                          (v > 0 || it + kk > 0) ? 1u : 0u);
-            }
-            umma_commit(smem_u32(&empty_bar[s]));
-            advance();
-          }
-          if (!ok) break;
-          umma_commit(smem_u32(&o_done[slot]));
-        }
+      return smem_u32(ring) + static_cast<uint32_t>(s * kTreeStageBytes);
+    };
+    auto release = [&] {
+      if (elected) umma_commit(smem_u32(&empty_bar[s]));
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1u;
       }
+    };
+    for (int b = 0; b <= nbc && ok; ++b) {
+      if (b < nbc) {
+        const int slot = b & 1;
+        if (b >= 2)
+          ok = __all_sync(0xffffffffu, wait_parity(smem_u32(&s_free[slot]), ((b - 2) >> 1) & 1,
+                                                   abort_flag));
+        const uint32_t d = tmem + static_cast<uint32_t>(slot * kSlotCols);
+#pragma unroll
+        for (int it = 0; it < kItems; ++it) {
+          const uint32_t k_lo = desc_lo(next(), 16);
+          if (!ok) break;
+          constexpr uint32_t idesc = k8 ? idesc_f8_f32(128, kSlotCols, false, false, false, false)
+                                        : idesc_bf16_f32(128, kSlotCols);
+          if (elected) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_words<k8>(d, k_lo + kk * 2u, kDescHiSw128, q_lo + it * (kRows * 8u) + kk * 2u,
+                             kDescHiSw128, idesc, it + kk > 0);
+          }
+          release();
+        }
+        if (!ok) break;
+        if (elected) umma_commit(smem_u32(&s_full[slot]));
+      }
+      if (b > 0) {
+        const int v = b - 1, slot = v & 1;
+        ok = __all_sync(0xffffffffu,
+                        wait_parity(smem_u32(&p_full[slot]), (v >> 1) & 1, abort_flag));
+        const uint32_t p_lo =
+            desc_lo(smem_u32(ps) + static_cast<uint32_t>(slot * Sh::kSlotBytes), 128);
+#pragma unroll
+        for (int it = 0; it < kItems; ++it) {
+          // bf16: 64 keys an item, its d halves 8 KB apart, 16 keys a step 2048 bytes
+          // on; 8 bits: 128 keys, 32 a step 4096 bytes on.  Weights: 2 or 4 core
+          // matrices on
+          const uint32_t v_lo = desc_lo(next(), k8 ? 0 : kTreeStageBytes / 2);
+          if (!ok) break;
+          constexpr uint32_t idesc =
+              k8 ? idesc_f8_f32(128, Sh::kParts * kRows, false, true, true, true)
+                 : idesc_bf16_f32(128, kRows, true, true);
+          if (elected) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_words<k8>(tmem + o_col, v_lo + kk * (k8 ? 256u : 128u), kDescHiSw128,
+                             p_lo + (it * 4 + kk) * (k8 ? 32u : 16u), kDescHiPlain, idesc,
+                             v > 0 || it + kk > 0);
+          }
+          release();
+        }
+        if (!ok) break;
+        if (elected) umma_commit(smem_u32(&o_done[slot]));
+      }
+    }
+    if (elected) {
       umma_commit(smem_u32(final_bar));
       drain_wait(smem_u32(final_bar), 0, 50ull * 1000ull * 1000ull);
     }
@@ -538,7 +580,10 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     const uint32_t bar_id = 1u + static_cast<uint32_t>(wg);
     const int row0 = grp * kRows;
     const int c0 = wg * kCols;
-    load_queries<kRows, k8, kSoftmax>(p, g, row0, qs, rf_s, st);
+    start_queries<kRows, k8, kSoftmax>(p, g, row0, qs, ps, st);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(q_sent));
+    finish_queries<kRows, k8, kSoftmax>(p, qs, ps, rf_s, st);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(q_bar));
@@ -577,23 +622,27 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&s_full[slot]), (b >> 1) & 1,
                                                      abort_flag));
       tc_fence_after();
-      const uint32_t s_at = tmem + lane_addr + static_cast<uint32_t>(slot * kRows + c0);
+      const uint32_t s_at = tmem + lane_addr + static_cast<uint32_t>(slot * kSlotCols + c0);
       // e: scores in base-2 units over the running maximum, which stays unless
       // some e passes kLazyLog2
       float2 e[kCols / 2];
       float over = kUnsetMax;
       auto scores = [&] {
-        uint32_t sv[kCols];
+        uint32_t sv[kCols], lo[kCols];
         if (ok) {
           tmem_ld16(s_at, sv);
+          if constexpr (k8) tmem_ld16(s_at + kRows, lo);
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) sv[j] = 0u;
+          for (int j = 0; j < kCols; ++j) sv[j] = lo[j] = 0u;
         }
 #pragma unroll
-        for (int j = 0; j < kCols / 2; ++j)
+        for (int j = 0; j < kCols / 2; ++j) {
           e[j] = make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
+          if constexpr (k8)
+            e[j] = add2(e[j], make_float2(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1])));
+        }
       };
       auto factor = [&](int j) {
         float2 f = make_float2(kscale, kscale);
@@ -662,15 +711,15 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
                                                          ((b - 1) >> 1) & 1, abort_flag));
           if (ok) {
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < kCols; c += 16) {
+#pragma unroll 1
+            for (int part = 0; part < Sh::kParts; ++part) {
               uint32_t o[16];
-              const uint32_t at = tmem + lane_addr + o_col + static_cast<uint32_t>(c0 + c);
+              const uint32_t at = tmem + lane_addr + o_col + static_cast<uint32_t>(part * kRows + c0);
               tmem_ld16(at, o);
               tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                o[j] = __float_as_uint(__uint_as_float(o[j]) * a_s[c0 + c + j]);
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * a_s[c0 + j]);
               tmem_st16(at, o);
             }
             tmem_wait_st();
@@ -737,18 +786,22 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     tc_fence_after();
     const float of = k8 ? pow2i(c_exp - kWeightShift) : 1.0f;
     float* po = p.part_o + (part * kRows + c0) * kAttnHeadDim + r;
+    float sum[16];
 #pragma unroll
-    for (int c = 0; c < kCols; c += 16) {
-      uint32_t o[16];
-      if (ok) {
-        tmem_ld16(tmem + lane_addr + o_col + static_cast<uint32_t>(c0 + c), o);
+    for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
+    if (ok) {
+#pragma unroll
+      for (int part = 0; part < Sh::kParts; ++part) {
+        uint32_t o[16];
+        tmem_ld16(tmem + lane_addr + o_col + static_cast<uint32_t>(part * kRows + c0), o);
         tmem_wait_ld();
-      }
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (row0 + c0 + c + j < p.R)
-          po[static_cast<size_t>(c + j) * kAttnHeadDim] = ok ? __uint_as_float(o[j]) * of : 0.0f;
+        for (int j = 0; j < 16; ++j) sum[j] += __uint_as_float(o[j]);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (row0 + c0 + j < p.R) po[static_cast<size_t>(j) * kAttnHeadDim] = sum[j] * of;
     tc_fence_before();
   }
   __syncthreads();

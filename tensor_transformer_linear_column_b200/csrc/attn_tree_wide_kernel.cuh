@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint64_t* full_bar = bars;                       // [kWideMaxStages]
   uint64_t* empty_bar = full_bar + kWideMaxStages; // [kWideMaxStages]
   uint64_t* q_bar = empty_bar + kWideMaxStages;
-  uint64_t* s_full = q_bar + 1;    // [tile] scores of a unit, P_t free, O_t up to date
+  uint64_t* q_sent = q_bar + 1;    // the queries' copies have been started
+  uint64_t* s_full = q_sent + 1;   // [tile] scores of a unit, P_t free, O_t up to date
   uint64_t* p_full = s_full + 2;   // [tile] weights written, O rescaled
   uint64_t* o_done = p_full + 2;   // [tile] the last unit's value product done
   uint64_t* final_bar = o_done + 2;
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     mbar_init(smem_u32(q_bar), 8);
+    mbar_init(smem_u32(q_sent), 8);
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&s_full[t]), 1);
       mbar_init(smem_u32(&p_full[t]), 4);
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint32_t issued = 0u, phases = 0u;
       int s = 0;
       uint32_t ph = 0u;
-      bool ok = true;
+      bool ok = wait_parity(smem_u32(q_sent), 0, abort_flag);
       auto load = [&](bool is_v, int b) {
         const int kb = key0 + b * 128;
         for (int it = 0; it < kItems && ok; ++it) {
@@ -180,85 +182,84 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer: units 0 and 1's scores, then unit i's values and
-      // unit i + 2's scores
-      bool ok = wait_parity(smem_u32(q_bar), 0, abort_flag);
+    // ---------------- MMA issuer: units 0 and 1's scores, then unit i's values and
+    // unit i + 2's scores.  One issuer for both tiles keeps them half a period apart;
+    // with one each they fell into step, and 64 tokens over 65536 rows took 205 us
+    // instead of ISSUER_FIGURE.
+    const bool elected = elect_one();
+    bool ok = __all_sync(0xffffffffu, wait_parity(smem_u32(q_bar), 0, abort_flag));
+    tc_fence_after();
+    const uint32_t q_lo = desc_lo(smem_u32(qs), 16), p_lo = desc_lo(smem_u32(ps), 16);
+    // the tile at position `pos` (item it) of the ring's order, once it has landed
+    auto landed = [&](int pos, int it, int& s) -> uint32_t {
+      const int n = pos * kItems + it;
+      s = n % kStages;
+      ok = ok && __all_sync(0xffffffffu, wait_parity(smem_u32(&full_bar[s]),
+                                                     static_cast<uint32_t>(n / kStages) & 1u,
+                                                     abort_flag));
       tc_fence_after();
-      auto stage_of = [&](int pos, int it, uint32_t& ph) -> int {
-        const int n = pos * kItems + it;
-        ph = static_cast<uint32_t>(n / kStages) & 1u;
-        return n % kStages;
-      };
-      auto scores = [&](int i) {
-        const int t = i & 1, b = kShared ? i >> 1 : i;
-        const uint32_t d = tmem + static_cast<uint32_t>(t * 128);
-        const uint32_t q = smem_u32(qs) + (kShared ? t * 32768u : 0u);
-        for (int it = 0; it < kItems && ok; ++it) {
-          uint32_t ph;
-          const int s = stage_of(k_pos(b), it, ph);
-          ok = wait_parity(smem_u32(&full_bar[s]), ph, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
-          if constexpr (k8) {
-            constexpr uint32_t idesc = idesc_f8_f32(128, 128, false, false, false, false);
+      return smem_u32(ring) + static_cast<uint32_t>(s * kTreeStageBytes);
+    };
+    auto scores = [&](int i) {
+      const int t = i & 1, b = kShared ? i >> 1 : i;
+      const uint32_t d = tmem + static_cast<uint32_t>(t * 128);
+      const uint32_t a_lo = q_lo + (kShared ? t * 2048u : 0u);
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+      for (int it = 0; it < kItems; ++it) {
+        int s;
+        const uint32_t k_lo = desc_lo(landed(k_pos(b), it, s), 16);
+        if (!ok) return;
+        constexpr uint32_t idesc = k8 ? idesc_f8_f32(128, 128, false, false, false, false)
+                                      : idesc_bf16_f32(128, 128);
+        if (elected) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_f8(d, desc_kmajor_sw128(q + part * 16384u + kk * 32u),
-                        desc_kmajor_sw128(st + kk * 32u), idesc, part + kk > 0 ? 1u : 0u);
-          } else {
-            constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+          for (int part = 0; part < (k8 ? 2 : 1); ++part)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_bf16(d, desc_kmajor_sw128(q + it * 16384u + kk * 32u),
-                        desc_kmajor_sw128(st + kk * 32u), idesc, it + kk > 0 ? 1u : 0u);
-          }
+              umma_words<k8>(d, a_lo + (it + part) * 1024u + kk * 2u, kDescHiSw128, k_lo + kk * 2u,
+                             kDescHiSw128, idesc, it + part + kk > 0);
           if (!kShared || t == 1) umma_commit(smem_u32(&empty_bar[s]));
         }
-        if (ok) umma_commit(smem_u32(&s_full[t]));
-      };
-      auto values = [&](int i) {
-        const int t = i & 1, b = kShared ? i >> 1 : i;
-        const bool first = i < 2;
-        ok = wait_parity(smem_u32(&p_full[t]), (i >> 1) & 1, abort_flag);
-        const uint32_t d = tmem + 256u + static_cast<uint32_t>(t * 128);
-        const uint32_t pb = smem_u32(ps) + static_cast<uint32_t>(t * Sh::kPBytes);
-        for (int it = 0; it < kItems && ok; ++it) {
-          uint32_t ph;
-          const int s = stage_of(v_pos(b), it, ph);
-          ok = wait_parity(smem_u32(&full_bar[s]), ph, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t st = smem_u32(ring + s * kTreeStageBytes);
-          if constexpr (k8) {
-            constexpr uint32_t idesc = idesc_f8_f32(128, 128, true, false, false, true);
-#pragma unroll
-            for (int part = 0; part < 3; ++part)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_f8(d, desc_kmajor_sw128(pb + part * 16384u + kk * 32u),
-                        desc_mnmajor_sw128(st + kk * 4096u, 0), idesc,
-                        (!first || part + kk > 0) ? 1u : 0u);
-          } else {
-            constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, true);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_bf16_ta(d, tmem + static_cast<uint32_t>(t * 128 + it * 32 + kk * 8),
-                           desc_mnmajor_sw128(st + kk * 2048u, kTreeStageBytes / 2), idesc,
-                           (!first || it + kk > 0) ? 1u : 0u);
-          }
-          if (!kShared || t == 1) umma_commit(smem_u32(&empty_bar[s]));
-        }
-        if (ok && i + 2 >= units) umma_commit(smem_u32(&o_done[t]));
-      };
-      for (int i = 0; i < 2 && i < units && ok; ++i) scores(i);
-      for (int i = 0; i < units && ok; ++i) {
-        values(i);
-        if (ok && i + 2 < units) scores(i + 2);
       }
+      if (elected) umma_commit(smem_u32(&s_full[t]));
+    };
+    auto values = [&](int i) {
+      const int t = i & 1, b = kShared ? i >> 1 : i;
+      ok = __all_sync(0xffffffffu, wait_parity(smem_u32(&p_full[t]), (i >> 1) & 1, abort_flag));
+      const uint32_t d = tmem + 256u + static_cast<uint32_t>(t * 128);
+      const uint32_t a_tmem = tmem + static_cast<uint32_t>(t * 128);
+      const uint32_t a_lo = p_lo + static_cast<uint32_t>(t * (Sh::kPBytes / 16));
+#pragma unroll
+      for (int it = 0; it < kItems; ++it) {
+        int s;
+        const uint32_t v_lo = desc_lo(landed(v_pos(b), it, s), k8 ? 0 : kTreeStageBytes / 2);
+        if (!ok) return;
+        constexpr uint32_t idesc = k8 ? idesc_f8_f32(128, 128, true, false, false, true)
+                                      : idesc_bf16_f32(128, 128, false, true);
+        if (elected) {
+#pragma unroll
+          for (int part = 0; part < (k8 ? 3 : 1); ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if constexpr (k8)
+                umma_words<true>(d, a_lo + part * 1024u + kk * 2u, kDescHiSw128, v_lo + kk * 256u,
+                                 kDescHiSw128, idesc, i >= 2 || part + kk > 0);
+              else
+                umma_words_ta(d, a_tmem + static_cast<uint32_t>(it * 32 + kk * 8),
+                              v_lo + kk * 128u, kDescHiSw128, idesc, i >= 2 || it + kk > 0);
+            }
+          if (!kShared || t == 1) umma_commit(smem_u32(&empty_bar[s]));
+        }
+      }
+      if (elected && i + 2 >= units) umma_commit(smem_u32(&o_done[t]));
+    };
+    if (ok) scores(0);
+    if (ok && units > 1) scores(1);
+    for (int i = 0; i < units && ok; ++i) {
+      values(i);
+      if (ok && i + 2 < units) scores(i + 2);
+    }
+    if (elected) {
       umma_commit(smem_u32(final_bar));
       drain_wait(smem_u32(final_bar), 0, 50ull * 1000ull * 1000ull);
     }
@@ -274,10 +275,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int r = q4 * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q4 * 32) << 16;
     const int row0 = grp * Sh::kTileRows + (kShared ? t * 128 : 0);
-    if constexpr (kShared)
-      load_queries<128, k8, 128>(p, g, row0, qs + t * 32768, rf_s + t * 128, st & 127);
-    else
-      load_queries<128, k8, 256>(p, g, row0, qs, rf_s, st);
+    constexpr int kQThreads = kShared ? 128 : 256;  // a tile's own rows, or both the same
+    const int qt = kShared ? st & 127 : st;
+    uint8_t* qd = qs + (kShared ? t * 32768 : 0);
+    start_queries<128, k8, kQThreads>(p, g, row0, qd, ps, qt);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(q_sent));
+    finish_queries<128, k8, kQThreads>(p, qd, ps, rf_s + (kShared ? t * 128 : 0), qt);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(q_bar));
