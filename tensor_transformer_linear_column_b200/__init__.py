@@ -9,6 +9,7 @@ is missing or fails to load, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -144,7 +145,7 @@ def _ptr_typed(t: Optional[torch.Tensor], name: str, dev: torch.device,
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
@@ -709,6 +710,13 @@ def tp_attn_tree_workspace_bytes(T: int, past: int, n_q_heads: int, n_kv_heads: 
                                                    int(n_kv_heads), int(head_dim)))
 
 
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(T: int, blocks: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """The workspace for `blocks` blocks of 128 cached tokens (the size depends on
+    `past` through them alone)."""
+    return tp_attn_tree_workspace_bytes(T, 128 * blocks, n_q_heads, n_kv_heads, head_dim)
+
+
 def _tree_call(name, qkv, cache_ptrs, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree,
                tree_mask, ctx, workspace, stream, dev) -> torch.Tensor:
     T = qkv.shape[0]
@@ -718,7 +726,7 @@ def _tree_call(name, qkv, cache_ptrs, max_len, past, n_q_heads, n_kv_heads, head
     else:
         _expect_shape(ctx, "ctx", (T, n_q_heads * head_dim))
     workspace = _workspace(
-        workspace, tp_attn_tree_workspace_bytes(T, past, n_q_heads, n_kv_heads, head_dim), qkv,
+        workspace, _tree_workspace(T, (past + 127) // 128, n_q_heads, n_kv_heads, head_dim), qkv,
         dev, stream)
     st = getattr(load(), name)(
         _ptr(qkv, "qkv", dev), *cache_ptrs, _ptr_typed(tree_mask, "tree_mask", dev, torch.int64), T,

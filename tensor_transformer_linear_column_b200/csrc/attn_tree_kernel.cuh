@@ -80,6 +80,7 @@ struct TreeParams {
   int nblk;         // key blocks of 128 in [0, past)
   int nb, chunks;   // key blocks per chunk, chunks per key-value head: grid x
   int max_len;
+  int append;       // this kernel writes the new rows (else the launch before it has)
   float scale_log2; // log2(e) / sqrt(d)
   const uint16_t* qkv;       // [T, (nq + 2 nkv) d]
   void* cache[2];            // K, V [nkv, max_len, d]: bf16 or E4M3 codes
@@ -301,39 +302,37 @@ __device__ __forceinline__ void finish_queries(const TreeParams& p, uint8_t* qs,
 }
 
 // The new tokens' K and V rows of head g behind the cached ones, the rows dealt
-// out over the head's blocks (block index `part` of `parts`), 16 lanes a row.
+// out over the head's blocks (block `part` of `parts`): one pass of the block's TMA
+// warp, two rows, from item `base` on.  The warp takes a pass after each key block
+// that it has sent for, so the rows cost the softmax warps nothing (in 8 bits their
+// divisions held up a call's first scores by 1.5 us).
 template <bool k8>
-__device__ __forceinline__ void append_rows(const TreeParams& p, int g, int part, int parts, int st,
-                                            int nthreads) {
-  const int l = st & 15;
-#pragma unroll 1
-  for (int base = 0; base < 2 * p.T; base += parts * (nthreads >> 4)) {
-    const int item = base + (st >> 4) * parts + part;  // (token, K or V)
-    const bool in = item < 2 * p.T;
-    if (!__any_sync(0xffffffffu, in)) continue;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (in)
-      raw = __ldg(reinterpret_cast<const uint4*>(
-                      p.qkv + (static_cast<size_t>(item >> 1) * (p.nq + 2 * p.nkv) + p.nq +
-                               (item & 1) * p.nkv + g) * kAttnHeadDim) +
-                  l);
-    const size_t row = static_cast<size_t>(g) * p.max_len + p.past + (item >> 1);
-    void* cache = item & 1 ? p.cache[1] : p.cache[0];
-    if constexpr (!k8) {
-      if (in)
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + row * kAttnHeadDim)[l] = raw;
-    } else {
-      float x[8];
-      unpack8(raw, x);
-      float amax = abs_max8(x);
+__device__ __forceinline__ void append_pass(const TreeParams& p, int g, int part, int parts,
+                                            int base, int lane) {
+  const int l = lane & 15;
+  const int item = base + (lane >> 4) * parts + part;  // (token, K or V)
+  const bool in = item < 2 * p.T;
+  uint4 raw = make_uint4(0, 0, 0, 0);
+  if (in)
+    raw = __ldg(reinterpret_cast<const uint4*>(
+                    p.qkv + (static_cast<size_t>(item >> 1) * (p.nq + 2 * p.nkv) + p.nq +
+                             (item & 1) * p.nkv + g) * kAttnHeadDim) +
+                l);
+  const size_t row = static_cast<size_t>(g) * p.max_len + p.past + (item >> 1);
+  void* cache = item & 1 ? p.cache[1] : p.cache[0];
+  if constexpr (!k8) {
+    if (in) reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + row * kAttnHeadDim)[l] = raw;
+  } else {
+    float x[8];
+    unpack8(raw, x);
+    float amax = abs_max8(x);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      float scale;
-      const uint2 codes = kv8_codes(x, amax, scale);
-      if (in) {
-        reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * kAttnHeadDim)[l] = codes;
-        if (l == 0) (item & 1 ? p.cache_scale[1] : p.cache_scale[0])[row] = scale;
-      }
+    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    float scale;
+    const uint2 codes = kv8_codes(x, amax, scale);
+    if (in) {
+      reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * kAttnHeadDim)[l] = codes;
+      if (l == 0) (item & 1 ? p.cache_scale[1] : p.cache_scale[0])[row] = scale;
     }
   }
 }
@@ -438,51 +437,59 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
   constexpr int kSlotCols = Sh::kScoreParts * kRows;
 
   if (warp == 0) {
+    // ---------------- TMA producer (lane 0), and the new rows
+    const int parts = p.chunks * p.groups, part = chunk + p.chunks * grp;
+    int append = p.append ? 0 : 2 * p.T;
     if (lane == 0) {
-      // ---------------- TMA producer
       prefetch_tmap(&tmap_k);
       prefetch_tmap(&tmap_v);
-      grid_dependency_wait();  // a preceding kernel may still write the cache
-      fence_proxy_async_global();
-      uint32_t issued = 0u, phases = 0u;
-      int s = 0;
-      uint32_t ph = 0u;
-      bool ok = wait_parity(smem_u32(q_sent), 0, abort_flag);
-      auto load = [&](bool is_v, int b) {
-        const int kb = key0 + b * 128;
-        for (int it = 0; it < kItems && ok; ++it) {
-          if (!wait_parity(smem_u32(&empty_bar[s]), ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = smem_u32(&full_bar[s]);
-          const uint32_t dst = smem_u32(ring + s * kTreeStageBytes);
-          mbar_arrive_expect_tx(fb, kTreeStageBytes);
-          if constexpr (k8) {
-            tma_load_3d(dst, is_v ? &tmap_v : &tmap_k, fb, 0, kb, g);
-          } else if (!is_v) {  // item: one 64-wide half of d, 128 keys
-            tma_load_3d(dst, &tmap_k, fb, it * 64, kb, g);
-          } else {             // item: 64 keys, both halves of d
-            tma_load_3d(dst, &tmap_v, fb, 0, kb + it * 64, g);
-            tma_load_3d(dst + kTreeStageBytes / 2, &tmap_v, fb, 64, kb + it * 64, g);
-          }
-          issued |= 1u << s;
-          phases = (phases & ~(1u << s)) | (ph << s);
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
+    }
+    grid_dependency_wait();  // a preceding kernel may still write the cache, or qkv
+    fence_proxy_async_global();
+    uint32_t issued = 0u, phases = 0u;
+    int s = 0;
+    uint32_t ph = 0u;
+    bool ok = lane == 0 && wait_parity(smem_u32(q_sent), 0, abort_flag);
+    auto load = [&](bool is_v, int b) {
+      const int kb = key0 + b * 128;
+      for (int it = 0; it < kItems && ok; ++it) {
+        if (!wait_parity(smem_u32(&empty_bar[s]), ph ^ 1u, abort_flag)) {
+          ok = false;
+          break;
         }
-      };
-      for (int b = 0; b <= nbc && ok; ++b) {
+        const uint32_t fb = smem_u32(&full_bar[s]);
+        const uint32_t dst = smem_u32(ring + s * kTreeStageBytes);
+        mbar_arrive_expect_tx(fb, kTreeStageBytes);
+        if constexpr (k8) {
+          tma_load_3d(dst, is_v ? &tmap_v : &tmap_k, fb, 0, kb, g);
+        } else if (!is_v) {  // item: one 64-wide half of d, 128 keys
+          tma_load_3d(dst, &tmap_k, fb, it * 64, kb, g);
+        } else {             // item: 64 keys, both halves of d
+          tma_load_3d(dst, &tmap_v, fb, 0, kb + it * 64, g);
+          tma_load_3d(dst + kTreeStageBytes / 2, &tmap_v, fb, 64, kb + it * 64, g);
+        }
+        issued |= 1u << s;
+        phases = (phases & ~(1u << s)) | (ph << s);
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    };
+    for (int b = 0; b <= nbc; ++b) {
+      if (lane == 0) {
         if (b < nbc) load(false, b);
         if (b > 0) load(true, b - 1);
       }
-      if (*abort_flag) {
-        for (int st = 0; st < kStages; ++st)
-          if (issued & (1u << st))
-            drain_wait(smem_u32(&full_bar[st]), (phases >> st) & 1u, 50ull * 1000ull * 1000ull);
-      }
+      __syncwarp();
+      if (append < 2 * p.T) append_pass<k8>(p, g, part, parts, append, lane);
+      append += 2 * parts;
+    }
+    for (; append < 2 * p.T; append += 2 * parts) append_pass<k8>(p, g, part, parts, append, lane);
+    if (lane == 0 && *abort_flag) {
+      for (int st = 0; st < kStages; ++st)
+        if (issued & (1u << st))
+          drain_wait(smem_u32(&full_bar[st]), (phases >> st) & 1u, 50ull * 1000ull * 1000ull);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -587,7 +594,6 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(q_bar));
-    append_rows<k8>(p, g, chunk + p.chunks * grp, p.chunks * p.groups, st, kSoftmax);
     if (et < kCols) nm_s[c0 + et] = -kUnsetMax;
     named_barrier_sync(5, kSoftmax);  // rf_s and nm_s are written
 
@@ -817,7 +823,7 @@ struct TreeMergeParams {
   int warps;        // warps per (token, query head): 1, 2, 4 or 8
   float scale;      // 1 / sqrt(d)
   const uint16_t* qkv;
-  const void* cache[2];
+  const uint8_t* cache[2];         // 8 bits: the caches, for the new rows
   const float* cache_scale[2];
   const unsigned long long* mask;  // [T][words], or null: j <= i
   const float* part_o;
@@ -860,18 +866,7 @@ __device__ __forceinline__ void merge_add(MergeState& a, float w, const float4& 
   a.o.w = fmaf(w, v.w, a.o.w);
 }
 
-// Four elements of a cached row.
-template <bool k8>
-__device__ __forceinline__ uint2 cache_raw(const void* cache, size_t row, int lane) {
-  if constexpr (k8)
-    return make_uint2(__ldcg(reinterpret_cast<const unsigned int*>(
-                                 static_cast<const uint8_t*>(cache) + row * kAttnHeadDim) + lane),
-                      0u);
-  else
-    return __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(cache) +
-                                                 row * kAttnHeadDim) + lane);
-}
-
+// Four elements of a row.
 template <bool k8>
 __device__ __forceinline__ float4 cache_values(const uint2& raw) {
   if constexpr (k8) {
@@ -888,14 +883,13 @@ __device__ __forceinline__ float4 cache_values(const uint2& raw) {
 
 // p.warps warps per (token, query head).  Warp w takes the visible new tokens
 // j = w, w + warps, ..., four at a time, and then chunks w, w + warps, ..., four
-// at a time, in order, the first chunks' loads issued before all else; the warps'
-// states are then added in order.  Bit-identical from run to run.
+// at a time, in order; the warps' states are then added in order.  Bit-identical
+// from run to run.
 template <bool k8>
 __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     attn_tree_merge_kernel(const TreeMergeParams p) {
   __shared__ float4 red_o[kMergeWarps][32];
   __shared__ float red_l[kMergeWarps], red_m[kMergeWarps];
-  grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = warp & (p.warps - 1);
   const int wid = (blockIdx.x * kMergeWarps + warp) / p.warps;
@@ -908,6 +902,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     const int rr = i * p.G + h - g * p.G;
     const int grp = rr / p.rows, n = rr - grp * p.rows;
     const size_t base = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks * p.rows + n;
+    // qkv and the mask are complete: the preceding kernel has waited for them
+    // before it let this one start
+    const float f = p.scale * 1.4426950408889634f;
+    const size_t ld = static_cast<size_t>(p.nq + 2 * p.nkv) * kAttnHeadDim;
+    const float4 q = cache_values<false>(
+        __ldg(reinterpret_cast<const uint2*>(p.qkv + i * ld + h * kAttnHeadDim) + lane));
+    const unsigned long long mine =
+        (p.warps == 8 ? 0x0101010101010101ull : p.warps == 4 ? 0x1111111111111111ull
+         : p.warps == 2 ? 0x5555555555555555ull : ~0ull) << w;
+    const size_t row0 = static_cast<size_t>(g) * p.max_len + p.past;
     float2 ml[kMergeChunks];
     float4 o[kMergeChunks];
     auto load_chunks = [&](int c0) {
@@ -923,17 +927,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
         }
       }
     };
-    load_chunks(w);
-    // the new tokens that row i sees
-    const float f = p.scale * 1.4426950408889634f;
-    const float4 q = cache_values<false>(
-        __ldg(reinterpret_cast<const uint2*>(
-                  p.qkv + (static_cast<size_t>(i) * (p.nq + 2 * p.nkv) + h) * kAttnHeadDim) +
-              lane));
-    const unsigned long long mine =
-        (p.warps == 8 ? 0x0101010101010101ull : p.warps == 4 ? 0x1111111111111111ull
-         : p.warps == 2 ? 0x5555555555555555ull : ~0ull) << w;
-    const size_t row0 = static_cast<size_t>(g) * p.max_len + p.past;
+    if constexpr (k8) {
+      grid_dependency_wait();  // the new rows' codes, and the partials
+      grid_launch_dependents();
+      load_chunks(w);
+    }
+    // the new tokens that row i sees: bf16 from qkv, before the wait; 8 bits as
+    // they were written
     for (int word = 0; word < p.words; ++word) {
       const int left = p.T - word * 64;                       // tokens from this word on
       unsigned long long bits = left >= 64 ? ~0ull : (1ull << left) - 1ull;
@@ -955,8 +955,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
           if (bits != 0ull) {
             const int j = word * 64 + __ffsll(static_cast<long long>(bits)) - 1;
             bits &= bits - 1ull;
-            kr[k] = cache_raw<k8>(p.cache[0], row0 + j, lane);
-            vr[k] = cache_raw<k8>(p.cache[1], row0 + j, lane);
+            if constexpr (k8) {
+              kr[k].x = __ldcg(reinterpret_cast<const unsigned int*>(
+                                   p.cache[0] + (row0 + j) * kAttnHeadDim) + lane);
+              vr[k].x = __ldcg(reinterpret_cast<const unsigned int*>(
+                                   p.cache[1] + (row0 + j) * kAttnHeadDim) + lane);
+            } else {
+              const uint16_t* at = p.qkv + j * ld + (p.nq + g) * kAttnHeadDim;
+              kr[k] = __ldg(reinterpret_cast<const uint2*>(at) + lane);
+              vr[k] = __ldg(reinterpret_cast<const uint2*>(at + p.nkv * kAttnHeadDim) + lane);
+            }
             if (k8 && slot == k) {
               ks = __ldcg(p.cache_scale[0] + row0 + j);
               vs = __ldcg(p.cache_scale[1] + row0 + j);
@@ -983,8 +991,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
         }
       }
     }
+    if constexpr (!k8) {
+      grid_dependency_wait();  // the partials
+      grid_launch_dependents();
+    }
     for (int c0 = w; c0 < p.chunks; c0 += p.warps * kMergeChunks) {
-      if (c0 != w) load_chunks(c0);
+      if (!k8 || c0 != w) load_chunks(c0);
       float high = ml[0].x;
 #pragma unroll
       for (int k = 1; k < kMergeChunks; ++k) high = fmaxf(high, ml[k].x);
@@ -999,6 +1011,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     // the new tokens' sum over their slots
     st.lt += __shfl_xor_sync(0xffffffffu, st.lt, 8);
     st.l += st.lt + __shfl_xor_sync(0xffffffffu, st.lt, 16);
+  } else {
+    grid_dependency_wait();
   }
   if (p.warps > 1) {
     red_o[warp][lane] = st.o;

@@ -132,53 +132,62 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t tmem = *tmem_slot;  // S_0, S_1 at columns 0 and 128, O_0, O_1 at 256, 384
 
   if (warp == 0) {
+    // ---------------- TMA producer (lane 0), and the new rows
+    const int parts = p.chunks * p.groups, part = chunk + p.chunks * grp;
+    int append = p.append ? 0 : 2 * p.T;
     if (lane == 0) {
-      // ---------------- TMA producer
       prefetch_tmap(&tmap_k);
       prefetch_tmap(&tmap_v);
-      grid_dependency_wait();  // a preceding kernel may still write the cache
-      fence_proxy_async_global();
-      uint32_t issued = 0u, phases = 0u;
-      int s = 0;
-      uint32_t ph = 0u;
-      bool ok = wait_parity(smem_u32(q_sent), 0, abort_flag);
-      auto load = [&](bool is_v, int b) {
-        const int kb = key0 + b * 128;
-        for (int it = 0; it < kItems && ok; ++it) {
-          if (!wait_parity(smem_u32(&empty_bar[s]), ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = smem_u32(&full_bar[s]);
-          const uint32_t dst = smem_u32(ring + s * kTreeStageBytes);
-          mbar_arrive_expect_tx(fb, kTreeStageBytes);
-          if constexpr (k8) {
-            tma_load_3d(dst, is_v ? &tmap_v : &tmap_k, fb, 0, kb, g);
-          } else if (!is_v) {  // item: one 64-wide half of d, 128 keys
-            tma_load_3d(dst, &tmap_k, fb, it * 64, kb, g);
-          } else {             // item: 64 keys, both halves of d
-            tma_load_3d(dst, &tmap_v, fb, 0, kb + it * 64, g);
-            tma_load_3d(dst + kTreeStageBytes / 2, &tmap_v, fb, 64, kb + it * 64, g);
-          }
-          issued |= 1u << s;
-          phases = (phases & ~(1u << s)) | (ph << s);
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
+    }
+    grid_dependency_wait();  // a preceding kernel may still write the cache, or qkv
+    fence_proxy_async_global();
+    uint32_t issued = 0u, phases = 0u;
+    int s = 0;
+    uint32_t ph = 0u;
+    bool ok = lane == 0 && wait_parity(smem_u32(q_sent), 0, abort_flag);
+    auto load = [&](bool is_v, int b) {
+      const int kb = key0 + b * 128;
+      for (int it = 0; it < kItems && ok; ++it) {
+        if (!wait_parity(smem_u32(&empty_bar[s]), ph ^ 1u, abort_flag)) {
+          ok = false;
+          break;
         }
-      };
+        const uint32_t fb = smem_u32(&full_bar[s]);
+        const uint32_t dst = smem_u32(ring + s * kTreeStageBytes);
+        mbar_arrive_expect_tx(fb, kTreeStageBytes);
+        if constexpr (k8) {
+          tma_load_3d(dst, is_v ? &tmap_v : &tmap_k, fb, 0, kb, g);
+        } else if (!is_v) {  // item: one 64-wide half of d, 128 keys
+          tma_load_3d(dst, &tmap_k, fb, it * 64, kb, g);
+        } else {             // item: 64 keys, both halves of d
+          tma_load_3d(dst, &tmap_v, fb, 0, kb + it * 64, g);
+          tma_load_3d(dst + kTreeStageBytes / 2, &tmap_v, fb, 64, kb + it * 64, g);
+        }
+        issued |= 1u << s;
+        phases = (phases & ~(1u << s)) | (ph << s);
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    };
+    if (lane == 0)
       for (int x = 0; x < pre; ++x) load(false, x);
-      for (int x = 0; x < nbc && ok; ++x) {
+    for (int x = 0; x < nbc; ++x) {
+      if (lane == 0) {
         if (kShared && x + pre < nbc) load(false, x + pre);
         load(true, x);
         if (!kShared && x + pre < nbc) load(false, x + pre);
       }
-      if (*abort_flag) {
-        for (int st = 0; st < kStages; ++st)
-          if (issued & (1u << st))
-            drain_wait(smem_u32(&full_bar[st]), (phases >> st) & 1u, 50ull * 1000ull * 1000ull);
-      }
+      __syncwarp();
+      if (append < 2 * p.T) append_pass<k8>(p, g, part, parts, append, lane);
+      append += 2 * parts;
+    }
+    for (; append < 2 * p.T; append += 2 * parts) append_pass<k8>(p, g, part, parts, append, lane);
+    if (lane == 0 && *abort_flag) {
+      for (int st = 0; st < kStages; ++st)
+        if (issued & (1u << st))
+          drain_wait(smem_u32(&full_bar[st]), (phases >> st) & 1u, 50ull * 1000ull * 1000ull);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -285,7 +294,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(q_bar));
-    append_rows<k8>(p, g, chunk + p.chunks * grp, p.chunks * p.groups, st, 256);
     named_barrier_sync(3, 256);  // rf_s is written
     const float rf = k8 ? rf_s[(kShared ? t * 128 : 0) + r] : p.scale_log2;
     const int mine = kShared ? nbc : (nbc - t + 1) / 2;  // this tile's units

@@ -61,6 +61,7 @@ struct KvAppendParams {
 template <bool k8>
 __global__ void __launch_bounds__(kCacheThreads) kv_append_rows_kernel(const KvAppendParams p) {
   grid_dependency_wait();  // qkv comes from the preceding kernel
+  grid_launch_dependents();
   const int lane_in = threadIdx.x % p.lanes;
   const int g = blockIdx.y >> 1, which = blockIdx.y & 1;
   const int e0 = lane_in * 8;
@@ -104,7 +105,6 @@ __global__ void __launch_bounds__(kCacheThreads) kv_append_rows_kernel(const KvA
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + row * p.d + e0) = raw[b];
     }
   }
-  grid_launch_dependents();
 }
 
 struct Kv8ReadParams {
@@ -120,6 +120,7 @@ constexpr int kReadBatch = 4;
 // thread turns 16 codes (one 16-byte load) into 32 bytes.
 __global__ void __launch_bounds__(kCacheThreads) kv8_read_kernel(const Kv8ReadParams p) {
   grid_dependency_wait();
+  grid_launch_dependents();
   const int g = blockIdx.y >> 1, which = blockIdx.y & 1;
   const int per_row = p.d / 16;
   const long long pieces = static_cast<long long>(p.count) * per_row;
@@ -159,7 +160,6 @@ __global__ void __launch_bounds__(kCacheThreads) kv8_read_kernel(const Kv8ReadPa
       }
     }
   }
-  grid_launch_dependents();
 }
 
 }  // namespace tpb

@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_kernel(const QkPar
   }
   __syncthreads();
   grid_dependency_wait();  // qkv comes from the preceding kernel
+  grid_launch_dependents();
 
   const int h0 = blockIdx.y * p.seg;  // this block's heads
   const int n = p.heads - h0 < p.seg ? p.heads - h0 : p.seg;
@@ -470,7 +471,6 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_kernel(const QkPar
     }
   }
   __syncthreads();
-  grid_launch_dependents();
 }
 
 // The gains' gradients: column (kind, element) of partial [blocks][2 d] summed
@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(16 * kQkReduceLanes)
                           uint16_t* __restrict__ dgamma_q, uint16_t* __restrict__ dgamma_k) {
   __shared__ float sums[kQkReduceLanes][16];
   grid_dependency_wait();
+  grid_launch_dependents();
   const int col = blockIdx.x * 16 + (threadIdx.x & 15);  // d is a multiple of 16
   const int part = threadIdx.x >> 4;
   float s = 0.0f;
@@ -495,7 +496,6 @@ __global__ void __launch_bounds__(16 * kQkReduceLanes)
     const __nv_bfloat16 b = __float2bfloat16_rn(total);
     (col < d ? dgamma_q[col] : dgamma_k[col - d]) = *reinterpret_cast<const uint16_t*>(&b);
   }
-  grid_launch_dependents();
 }
 
 }  // namespace tpb

@@ -958,8 +958,29 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + po);
   cudaLaunchAttribute attr[1];
+  // The new keys and values are written by the blocks of the next launch, two rows a
+  // pass and head; where each would take more than four passes (about 1 us each),
+  // and where there is nothing cached, by a launch of their own (2 us).
+  p.append = past > 0 && T <= 4 * p.chunks * p.groups ? 1 : 0;
+  if (!p.append) {
+    tpb::KvAppendParams a{};
+    a.qkv = qkv;
+    a.cache[0] = k_cache;
+    a.cache[1] = v_cache;
+    a.scale[0] = k_scale;
+    a.scale[1] = v_scale;
+    a.T = a.n = T;
+    a.past = past;
+    a.max_len = max_len;
+    a.nq = nq;
+    a.nkv = nkv;
+    a.d = d;
+    a.lanes = row_lanes(d);
+    const tp_status s = launch_append<k8>(a, stream);
+    if (s != TP_OK) return s;
+  }
   if (past > 0) {
-    // 1. the cached keys, chunk by chunk, and the new keys and values behind them
+    // 1. the cached keys, chunk by chunk
     CUtensorMap tk, tv;
     const uint64_t outer = static_cast<uint64_t>(max_len) * d;
     const bool maps =
@@ -978,22 +999,6 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
                       l.threads, l.smem, stream, attr);
     if (!cuda_ok(cudaLaunchKernelEx(&cfg, l.kernel, tk, tv, p), "launch attn_tree_kernel"))
       return TP_ERR_CUDA;
-  } else {
-    tpb::KvAppendParams a{};
-    a.qkv = qkv;
-    a.cache[0] = k_cache;
-    a.cache[1] = v_cache;
-    a.scale[0] = k_scale;
-    a.scale[1] = v_scale;
-    a.T = a.n = T;
-    a.past = past;
-    a.max_len = max_len;
-    a.nq = nq;
-    a.nkv = nkv;
-    a.d = d;
-    a.lanes = row_lanes(d);
-    const tp_status s = launch_append<k8>(a, stream);
-    if (s != TP_OK) return s;
   }
   // 2. the partials and the new tokens that each row sees
   tpb::TreeMergeParams m{};
@@ -1008,8 +1013,8 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
   m.words = (T + 63) / 64;
   m.scale = 1.0f / sqrtf(static_cast<float>(d));
   m.qkv = qkv;
-  m.cache[0] = k_cache;
-  m.cache[1] = v_cache;
+  m.cache[0] = static_cast<const uint8_t*>(k_cache);
+  m.cache[1] = static_cast<const uint8_t*>(v_cache);
   m.cache_scale[0] = k_scale;
   m.cache_scale[1] = v_scale;
   m.mask = reinterpret_cast<const unsigned long long*>(mask);
