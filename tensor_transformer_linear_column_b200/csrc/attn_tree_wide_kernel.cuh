@@ -40,7 +40,7 @@ namespace tpb {
 
 constexpr int kWideThreads = 64 + 256;   // TMA warp, MMA warp, two softmax warpgroups
 constexpr int kWideMaxStages = 10;
-constexpr float kWideLazyLog2 = 16.0f;          // bf16: weights up to 2^16
+constexpr float kWideSumMax = 1048576.0f;       // bf16: 64 keys' sum of weights up to 2^20
 constexpr float kWideProductMax = 57344.0f;     // the largest E5M2 value
 constexpr float kWideProductLog2 = 5.0f;        // a raise leaves products up to 2^5
 constexpr float kWideSumMaxKv8 = 1.2676506e30f; // 2^100
@@ -81,8 +81,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint64_t* q_bar = empty_bar + kWideMaxStages;
   uint64_t* q_sent = q_bar + 1;    // the queries' copies have been started
   uint64_t* s_full = q_sent + 1;   // [tile] scores of a unit, P_t free, O_t up to date
-  uint64_t* p_full = s_full + 2;   // [tile] weights written, O rescaled
-  uint64_t* o_done = p_full + 2;   // [tile] the last unit's value product done
+  uint64_t* p_full = s_full + 2;   // [tile][half] weights written, O rescaled
+  uint64_t* h_done = p_full + 4;   // [tile] the first half's value product done
+  uint64_t* o_done = h_done + 2;   // [tile] the last unit's value product done
   uint64_t* final_bar = o_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -115,7 +116,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     mbar_init(smem_u32(q_sent), 8);
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&s_full[t]), 1);
-      mbar_init(smem_u32(&p_full[t]), 4);
+      mbar_init(smem_u32(&p_full[2 * t]), 4);
+      mbar_init(smem_u32(&p_full[2 * t + 1]), 4);
+      mbar_init(smem_u32(&h_done[t]), 1);
       mbar_init(smem_u32(&o_done[t]), 1);
     }
     mbar_init(smem_u32(final_bar), 1);
@@ -234,30 +237,35 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     };
     auto values = [&](int i) {
       const int t = i & 1, b = kShared ? i >> 1 : i;
-      ok = __all_sync(0xffffffffu, wait_parity(smem_u32(&p_full[t]), (i >> 1) & 1, abort_flag));
       const uint32_t d = tmem + 256u + static_cast<uint32_t>(t * 128);
       const uint32_t a_tmem = tmem + static_cast<uint32_t>(t * 128);
       const uint32_t a_lo = p_lo + static_cast<uint32_t>(t * (Sh::kPBytes / 16));
 #pragma unroll
-      for (int it = 0; it < kItems; ++it) {
+      for (int half = 0; half < 2; ++half) {  // 64 keys: one bf16 item, half an 8-bit one
+        ok = ok && __all_sync(0xffffffffu, wait_parity(smem_u32(&p_full[2 * t + half]),
+                                                       (i >> 1) & 1, abort_flag));
         int s;
-        const uint32_t v_lo = desc_lo(landed(v_pos(b), it, s), k8 ? 0 : kTreeStageBytes / 2);
+        const uint32_t v_lo =
+            desc_lo(landed(v_pos(b), k8 ? 0 : half, s), k8 ? 0 : kTreeStageBytes / 2);
         if (!ok) return;
         constexpr uint32_t idesc = k8 ? idesc_f8_f32(128, 128, true, false, false, true)
                                       : idesc_bf16_f32(128, 128, false, true);
         if (elected) {
+          if constexpr (k8) {
 #pragma unroll
-          for (int part = 0; part < (k8 ? 3 : 1); ++part)
+            for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if constexpr (k8)
+              for (int part = 0; part < 3; ++part)
                 umma_words<true>(d, a_lo + part * 1024u + kk * 2u, kDescHiSw128, v_lo + kk * 256u,
                                  kDescHiSw128, idesc, i >= 2 || part + kk > 0);
-              else
-                umma_words_ta(d, a_tmem + static_cast<uint32_t>(it * 32 + kk * 8),
-                              v_lo + kk * 128u, kDescHiSw128, idesc, i >= 2 || it + kk > 0);
-            }
-          if (!kShared || t == 1) umma_commit(smem_u32(&empty_bar[s]));
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_words_ta(d, a_tmem + static_cast<uint32_t>(half * 32 + kk * 8),
+                            v_lo + kk * 128u, kDescHiSw128, idesc, i >= 2 || half + kk > 0);
+          }
+          if (half == 0) umma_commit(smem_u32(&h_done[t]));
+          if ((!k8 || half == 1) && (!kShared || t == 1)) umma_commit(smem_u32(&empty_bar[s]));
         }
       }
       if (elected && i + 2 >= units) umma_commit(smem_u32(&o_done[t]));
@@ -359,125 +367,61 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
         }
       };
-      // the block's weights with the running m into P_t; their sum, and (8 bits) the
-      // largest product with a value scale
-      float2 acc = make_float2(0.0f, 0.0f);
-      float top = 0.0f;
-      auto weights32 = [&](const uint32_t (&sv)[32], int c, bool tail) {
-        float2 e[16];
-        scaled(sv, c, m, tail, e);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          e[j] = make_float2(exp2_fast(e[j].x), exp2_fast(e[j].y));
-          acc = add2(acc, e[j]);
-          if constexpr (k8) {
-            e[j] = mul2(e[j], *reinterpret_cast<const float2*>(ks + 128 + c + 2 * j));
-            top = fmaxf(top, fmaxf(e[j].x, e[j].y));
-          }
-        }
-        // bf16: over the scores, two keys a column (this lane's columns below c + 32
-        // have been read).  8 bits: three parts of 128-byte rows, 16-byte piece j at
-        // j ^ (r % 8)
-        if constexpr (k8) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint4 a4, b4, c4;
-            split_weights(e + 8 * h, a4, b4, c4);
-            uint8_t* at = pt + (((c / 16 + h) ^ sw) << 4);
-            *reinterpret_cast<uint4*>(at) = a4;
-            *reinterpret_cast<uint4*>(at + 16384) = b4;
-            *reinterpret_cast<uint4*>(at + 32768) = c4;
-          }
-        } else {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(e[j].x, e[j].y);
-          tmem_st16(s_at + static_cast<uint32_t>(c / 2), pk);
-        }
-      };
-      auto weights = [&](auto tail) {
-        uint32_t sa[32], sb[32];
-        acc = make_float2(0.0f, 0.0f);
-        top = 0.0f;
-        fetch(0, sa);
+      // The block's halves of 64 keys in turn: weights with the running m, their sum
+      // and (8 bits) the largest product with a value scale.  If the sum (the product)
+      // has left its range, m is raised and the half done again; its scores are still
+      // there, for bf16 weights wait in registers until they are known to be good.
+      // The first half's value product runs under the second half's exponentials.
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 64) {  // the next scores on their way meanwhile
-          tmem_wait_ld();
-          fetch(c + 32, sb);
-          weights32(sa, c, tail);
-          tmem_wait_ld();
-          if (c == 0) fetch(64, sa);
-          weights32(sb, c + 32, tail);
-        }
-      };
-      // raise m by the block's maximum where `need`; l and O follow
-      auto raise = [&](bool need, float high, float product) {
-        // 8 bits: products up to 2^5, and no weight above 2^60
-        float mn = k8 ? fmaxf(product - kWideProductLog2, high - 60.0f) : high;
-        mn = need ? fmaxf(m, mn) : m;
-        // in two steps: an 8-bit row's m may rise by more than fp32's exponents
-        const float half = exp2f(0.5f * (m - mn));
-        l = l * half * half;
-        m = mn;
-        if (k > 0 && ok) {  // O holds the products of the tile's earlier units
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(o_at + static_cast<uint32_t>(c), o);
-            tmem_wait_ld();
+      for (int half = 0; half < 2; ++half) {
+        const int base = half * 64;
+        float2 acc;
+        float top;
+        uint32_t pk[k8 ? 1 : 32];
+        auto weights32 = [&](const uint32_t (&sv)[32], int c, bool tail) {  // keys base + c ...
+          float2 e[16];
+          scaled(sv, base + c, m, tail, e);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * half * half);
-            tmem_st16(o_at + static_cast<uint32_t>(c), o);
+          for (int j = 0; j < 16; ++j) {
+            e[j] = make_float2(exp2_fast(e[j].x), exp2_fast(e[j].y));
+            acc = add2(acc, e[j]);
+            if constexpr (k8) {
+              e[j] = mul2(e[j], *reinterpret_cast<const float2*>(ks + 128 + base + c + 2 * j));
+              top = fmaxf(top, fmaxf(e[j].x, e[j].y));
+            } else {
+              pk[c / 2 + j] = pack_bf16x2(e[j].x, e[j].y);
+            }
           }
-          tmem_wait_st();
-        }
-      };
-      auto all_weights = [&] {
-        if (left < 128)
-          weights(std::true_type{});
-        else
-          weights(std::false_type{});
-      };
-      if constexpr (!k8) {
-        // the maximum first: the weights go over the scores.  m stays while no
-        // weight passes 2^kWideLazyLog2
-        float high = kUnsetMax;
-        uint32_t sa[32], sb[32];
-        fetch(0, sa);
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 64) {
-          tmem_wait_ld();
-          fetch(c + 32, sb);
-          if (left < 128) {
+          if constexpr (k8) {  // rows of 128 bytes, 16-byte piece j at j ^ (r % 8), in 3 parts
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j >= left) sa[j] = 0xff800000u;
+            for (int h = 0; h < 2; ++h) {
+              uint4 a4, b4, c4;
+              split_weights(e + 8 * h, a4, b4, c4);
+              uint8_t* at = pt + ((((base + c) / 16 + h) ^ sw) << 4);
+              *reinterpret_cast<uint4*>(at) = a4;
+              *reinterpret_cast<uint4*>(at + 16384) = b4;
+              *reinterpret_cast<uint4*>(at + 32768) = c4;
+            }
           }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(sa[j]));
+        };
+        auto weights = [&](auto tail) {
+          uint32_t sa[32], sb[32];
+          acc = make_float2(0.0f, 0.0f);
+          top = 0.0f;
+          fetch(base, sa);
           tmem_wait_ld();
-          if (c == 0) fetch(64, sa);
-          if (left < 128) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + 32 + j >= left) sb[j] = 0xff800000u;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(sb[j]));
-        }
-        high *= rf;
-        const bool need = high - m > kWideLazyLog2;
-        if (__any_sync(0xffffffffu, need)) raise(need, high, 0.0f);
-        all_weights();
-      } else {
-        bool need = k == 0, raised = false;
+          fetch(base + 32, sb);  // on their way meanwhile
+          weights32(sa, 0, tail);
+          tmem_wait_ld();
+          weights32(sb, 32, tail);
+        };
+        bool need = k + half == 0, raised = false;
         for (;;) {
           if (__any_sync(0xffffffffu, need)) {
             raised = true;
             float high = kUnsetMax, product = kUnsetMax;
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
+            for (int c = base; c < base + 64; c += 32) {
               uint32_t sv[32];
               float2 e[16];
               fetch(c, sv);
@@ -486,26 +430,62 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 high = fmaxf(high, fmaxf(e[j].x, e[j].y));
-                const float2 lv = *reinterpret_cast<const float2*>(ks + 256 + c + 2 * j);
-                product = fmaxf(product, fmaxf(e[j].x + lv.x, e[j].y + lv.y));
+                if constexpr (k8) {
+                  const float2 lv = *reinterpret_cast<const float2*>(ks + 256 + c + 2 * j);
+                  product = fmaxf(product, fmaxf(e[j].x + lv.x, e[j].y + lv.y));
+                }
               }
             }
-            raise(need, high, product);
+            // 8 bits: products up to 2^5, and no weight above 2^60
+            float mn = k8 ? fmaxf(product - kWideProductLog2, high - 60.0f) : high;
+            mn = need ? fmaxf(m, mn) : m;
+            // in two steps: an 8-bit row's m may rise by more than fp32's exponents
+            const float part = exp2f(0.5f * (m - mn));
+            l = l * part * part;
+            m = mn;
+            // O holds the products of the tile's earlier units and of this one's
+            // first half: wait for that one
+            if (half == 1)
+              ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&h_done[t]), k & 1, abort_flag));
+            if (k + half > 0 && ok) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 128; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_at + static_cast<uint32_t>(c), o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * part * part);
+                tmem_st16(o_at + static_cast<uint32_t>(c), o);
+              }
+              tmem_wait_st();
+            }
           }
-          all_weights();
+          if (left < 128)
+            weights(std::true_type{});
+          else
+            weights(std::false_type{});
           // (NaN raises once, for nothing)
-          need = !(top <= kWideProductMax) || !(acc.x + acc.y <= kWideSumMaxKv8);
+          const float sum = acc.x + acc.y;
+          need = k8 ? !(top <= kWideProductMax) || !(sum <= kWideSumMaxKv8) : !(sum <= kWideSumMax);
           if (raised || !__any_sync(0xffffffffu, need)) break;
         }
+        l += acc.x + acc.y;
+        if constexpr (k8) {
+          fence_proxy_async_smem();  // the weights are read by the MMA through the async proxy
+        } else {
+          // two keys a column, over scores that have been read
+#pragma unroll
+          for (int j = 0; j < 32; j += 16)
+            tmem_st16(s_at + static_cast<uint32_t>(half * 32 + j),
+                      *reinterpret_cast<const uint32_t(*)[16]>(pk + j));
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * t + half]));
       }
-      l += acc.x + acc.y;
-      if constexpr (k8)
-        fence_proxy_async_smem();  // the weights are read by the MMA through the async proxy
-      else
-        tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
     }
     // both tiles': the ring is used again below
     for (int x = 0; x < 2 && x < units; ++x)

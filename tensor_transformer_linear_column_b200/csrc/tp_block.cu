@@ -1545,7 +1545,7 @@ tp_status tp_kv8_read(const uint8_t* k_cache, const float* k_scale, const uint8_
   p.max_len = max_len;
   p.out_len = out_len;
   p.d = head_dim;
-  const long long pieces = static_cast<long long>(count) * (head_dim / 16);
+  const long long pieces = static_cast<long long>(count) * (head_dim / 8);
   const long long per_block = static_cast<long long>(tpb::kCacheThreads) * tpb::kReadBatch;
   const long long blocks = (pieces + per_block - 1) / per_block;
   cudaLaunchAttribute attr[1];
