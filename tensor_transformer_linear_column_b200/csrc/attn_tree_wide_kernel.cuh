@@ -26,10 +26,13 @@
 // that time.  Issuing a unit's scores before the value product of the tile's last
 // one (scores read early, weights held in registers until P_t is free) was slower:
 // WIDE_EARLY_FIGURES
-// 8-bit caches: queries in two E4M3 parts, weights (times the value scales) in
-// three E5M2 parts, as in attn_tree_kernel; here a row's m bounds the products
-// p * scale themselves, so a key of a large value scale and a small weight costs
-// the others nothing.
+// 8-bit caches: scores as in attn_tree_kernel (queries in two E4M3 parts against
+// the codes); here two more warps turn each block's value codes into fp16 once for
+// all rows, and a row's weights times the value scales are fp16 against those
+// (relative error 2^-11; splitting them into three E5M2 terms, as for few rows, costs
+// three of eight instructions an element: 266 us instead of KV8_FIGURE for 64
+// tokens over 65536 rows).  A row's m bounds the products p * scale themselves, so a
+// key of a large value scale and a small weight costs the others nothing.
 #pragma once
 
 #include <type_traits>
@@ -38,10 +41,12 @@
 
 namespace tpb {
 
-constexpr int kWideThreads = 64 + 256;   // TMA warp, MMA warp, two softmax warpgroups
+// TMA warp, MMA warp, (8 bits) two converting warps, two softmax warpgroups
+__host__ __device__ constexpr int wide_first(bool k8) { return k8 ? 4 : 2; }
+__host__ __device__ constexpr int wide_threads(bool k8) { return 32 * wide_first(k8) + 256; }
 constexpr int kWideMaxStages = 10;
 constexpr float kWideSumMax = 1048576.0f;       // bf16: 64 keys' sum of weights up to 2^20
-constexpr float kWideProductMax = 57344.0f;     // the largest E5M2 value
+constexpr float kWideProductMax = 60000.0f;     // 8 bits: products are fp16
 constexpr float kWideProductLog2 = 5.0f;        // a raise leaves products up to 2^5
 constexpr float kWideSumMaxKv8 = 1.2676506e30f; // 2^100
 
@@ -50,18 +55,18 @@ struct WideShape {
   static constexpr int kKItems = k8 ? 1 : 2;            // stages per K (and per V) block
   static constexpr int kTileRows = kShared ? 256 : 128; // rows of a block
   static constexpr int kQBytes = (kShared ? 2 : 1) * 32768;
-  static constexpr int kPBytes = k8 ? 3 * 16384 : 0;      // one tile's weights in shared memory
+  static constexpr int kValueBytes = k8 ? 2 * 32768 : 0;  // two blocks' values as fp16
   static constexpr int kScaleBytes = k8 ? 2 * 2 * 3 * 128 * 4 : 0;  // [tile][slot][3][128]
   static constexpr int kSmallBytes = kScaleBytes + 256 * 4 + 384;
   static constexpr int kFit =
-      (227 * 1024 - 1024 - kSmallBytes - kQBytes - 2 * kPBytes) / kTreeStageBytes;
+      (227 * 1024 - 1024 - kSmallBytes - kQBytes - kValueBytes) / kTreeStageBytes;
   static constexpr int kStages = kFit > kWideMaxStages ? kWideMaxStages : kFit;
-  static constexpr int kSmem = 1024 + kStages * kTreeStageBytes + kQBytes + 2 * kPBytes + kSmallBytes;
-  static_assert(kStages >= 2 * kKItems + 1, "K and V of a block and the next K in flight");
+  static constexpr int kSmem = 1024 + kStages * kTreeStageBytes + kQBytes + kValueBytes + kSmallBytes;
+  static_assert(kStages >= 4 && kStages >= 2 * kKItems + 1, "K and V of a block and the next K in flight");
 };
 
 template <bool k8, bool kShared>
-__global__ void __launch_bounds__(kWideThreads, 1)
+__global__ void __launch_bounds__(wide_threads(k8), 1)
     attn_tree_wide_kernel(const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
   using Sh = WideShape<k8, kShared>;
@@ -72,8 +77,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem;
   uint8_t* qs = ring + kStages * kTreeStageBytes;
-  uint8_t* ps = qs + Sh::kQBytes;                                 // [tile]
-  float* rf_s = reinterpret_cast<float*>(ps + 2 * Sh::kPBytes);   // [256] score factors
+  uint8_t* vs = qs + Sh::kQBytes;                                // 8 bits: [2][2 x 64 keys]
+  float* rf_s = reinterpret_cast<float*>(vs + Sh::kValueBytes);  // [256] score factors
   float* sc_s = rf_s + 256;                                       // 8 bits: [tile][slot][3][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sc_s + Sh::kScaleBytes / 4);
   uint64_t* full_bar = bars;                       // [kWideMaxStages]
@@ -84,7 +89,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   uint64_t* p_full = s_full + 2;   // [tile][half] weights written, O rescaled
   uint64_t* h_done = p_full + 4;   // [tile] the first half's value product done
   uint64_t* o_done = h_done + 2;   // [tile] the last unit's value product done
-  uint64_t* final_bar = o_done + 2;
+  uint64_t* v_full = o_done + 2;   // [2] 8 bits: a block's values are fp16
+  uint64_t* v_free = v_full + 2;   // [2] and have been read
+  uint64_t* final_bar = v_free + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -119,6 +126,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(smem_u32(&p_full[2 * t]), 4);
       mbar_init(smem_u32(&p_full[2 * t + 1]), 4);
       mbar_init(smem_u32(&h_done[t]), 1);
+      mbar_init(smem_u32(&v_full[t]), 1);
+      mbar_init(smem_u32(&v_free[t]), 1);
       mbar_init(smem_u32(&o_done[t]), 1);
     }
     mbar_init(smem_u32(final_bar), 1);
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const bool elected = elect_one();
     bool ok = __all_sync(0xffffffffu, wait_parity(smem_u32(q_bar), 0, abort_flag));
     tc_fence_after();
-    const uint32_t q_lo = desc_lo(smem_u32(qs), 16), p_lo = desc_lo(smem_u32(ps), 16);
+    const uint32_t q_lo = desc_lo(smem_u32(qs), 16);
     // the tile at position `pos` (item it) of the ring's order, once it has landed
     auto landed = [&](int pos, int it, int& s) -> uint32_t {
       const int n = pos * kItems + it;
@@ -239,33 +248,38 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int t = i & 1, b = kShared ? i >> 1 : i;
       const uint32_t d = tmem + 256u + static_cast<uint32_t>(t * 128);
       const uint32_t a_tmem = tmem + static_cast<uint32_t>(t * 128);
-      const uint32_t a_lo = p_lo + static_cast<uint32_t>(t * (Sh::kPBytes / 16));
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // 64 keys: one bf16 item, half an 8-bit one
+      for (int half = 0; half < 2; ++half) {  // 64 keys, d halves 8 KB apart
         ok = ok && __all_sync(0xffffffffu, wait_parity(smem_u32(&p_full[2 * t + half]),
                                                        (i >> 1) & 1, abort_flag));
-        int s;
-        const uint32_t v_lo =
-            desc_lo(landed(v_pos(b), k8 ? 0 : half, s), k8 ? 0 : kTreeStageBytes / 2);
+        int s = 0;
+        uint32_t tile;
+        if constexpr (k8) {
+          if (half == 0)
+            ok = ok && __all_sync(0xffffffffu, wait_parity(smem_u32(&v_full[b & 1]), (b >> 1) & 1,
+                                                           abort_flag));
+          tc_fence_after();
+          tile = smem_u32(vs) + static_cast<uint32_t>((b & 1) * 32768 + half * 16384);
+        } else {
+          tile = landed(v_pos(b), half, s);
+        }
+        const uint32_t v_lo = desc_lo(tile, kTreeStageBytes / 2);
         if (!ok) return;
-        constexpr uint32_t idesc = k8 ? idesc_f8_f32(128, 128, true, false, false, true)
-                                      : idesc_bf16_f32(128, 128, false, true);
+        // A in tensor memory, B MN-major: both fp16, or both bf16
+        constexpr uint32_t idesc =
+            idesc_bf16_f32(128, 128, false, true) & ~(k8 ? (1u << 7) | (1u << 10) : 0u);
         if (elected) {
-          if constexpr (k8) {
 #pragma unroll
-            for (int kk = 2 * half; kk < 2 * half + 2; ++kk)
-#pragma unroll
-              for (int part = 0; part < 3; ++part)
-                umma_words<true>(d, a_lo + part * 1024u + kk * 2u, kDescHiSw128, v_lo + kk * 256u,
-                                 kDescHiSw128, idesc, i >= 2 || part + kk > 0);
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_words_ta(d, a_tmem + static_cast<uint32_t>(half * 32 + kk * 8),
-                            v_lo + kk * 128u, kDescHiSw128, idesc, i >= 2 || half + kk > 0);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            umma_words_ta(d, a_tmem + static_cast<uint32_t>(half * 32 + kk * 8), v_lo + kk * 128u,
+                          kDescHiSw128, idesc, i >= 2 || half + kk > 0);
           if (half == 0) umma_commit(smem_u32(&h_done[t]));
-          if ((!k8 || half == 1) && (!kShared || t == 1)) umma_commit(smem_u32(&empty_bar[s]));
+          if (!kShared || t == 1) {
+            if constexpr (!k8)
+              umma_commit(smem_u32(&empty_bar[s]));
+            else if (half == 1)
+              umma_commit(smem_u32(&v_free[b & 1]));
+          }
         }
       }
       if (elected && i + 2 >= units) umma_commit(smem_u32(&o_done[t]));
@@ -281,12 +295,50 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       drain_wait(smem_u32(final_bar), 0, 50ull * 1000ull * 1000ull);
     }
     __syncwarp();
+  } else if (k8 && warp < 4) {
+    // ---------------- value codes to fp16: [key][d] codes (16-byte chunk c of a row at
+    // c ^ (key % 8)) to the bf16 cache's tiles: per 64 keys two d halves of 128-byte rows
+    // (chunk j at j ^ (key % 8)).  A quarter warp takes chunks 0 .. 3 of a half of keys
+    // k and k ^ 5: these differ in the bits that keep its loads and its stores apart
+    // in the banks.
+    const int c4 = lane & 3, k8th = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+    bool ok = wait_parity(smem_u32(q_bar), 0, abort_flag);  // the queries were split in `vs`
+    for (int b = 0; b < nbc; ++b) {  // all of them: both warps take every barrier
+      const int n = v_pos(b);
+      const int s = n % kStages;
+      ok = ok && wait_parity(smem_u32(&full_bar[s]), static_cast<uint32_t>(n / kStages) & 1u,
+                             abort_flag);
+      if (b >= 2)
+        ok = ok && wait_parity(smem_u32(&v_free[b & 1]), ((b - 2) >> 1) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      const uint8_t* src = ring + s * kTreeStageBytes;
+      uint8_t* dst = vs + (b & 1) * 32768;
+#pragma unroll 4
+      for (int i = warp - 2; i < 32 && ok; i += 2) {
+        const int key = (i >> 1) * 8 + k8th, dh = i & 1;
+        const uint4 codes =
+            *reinterpret_cast<const uint4*>(src + key * 128 + (((dh * 4 + c4) ^ (key & 7)) << 4));
+        uint8_t* at = dst + (key >> 6) * 16384 + dh * 8192 + (key & 63) * 128;
+        *reinterpret_cast<uint4*>(at + (((2 * c4) ^ (key & 7)) << 4)) =
+            make_uint4(half2_of_e4m3x2(codes.x), half2_of_e4m3x2(codes.x >> 16),
+                       half2_of_e4m3x2(codes.y), half2_of_e4m3x2(codes.y >> 16));
+        *reinterpret_cast<uint4*>(at + (((2 * c4 + 1) ^ (key & 7)) << 4)) =
+            make_uint4(half2_of_e4m3x2(codes.z), half2_of_e4m3x2(codes.z >> 16),
+                       half2_of_e4m3x2(codes.w), half2_of_e4m3x2(codes.w >> 16));
+      }
+      fence_proxy_async_smem();  // read by the MMA through the async proxy
+      named_barrier_sync(4, 64);
+      if (ok && threadIdx.x == 64) {
+        mbar_arrive(smem_u32(&v_full[b & 1]));
+        mbar_arrive(smem_u32(&empty_bar[s]));
+      }
+    }
   } else {
     // ---------------- softmax: thread r of tile t owns its query row r.  Every
     // thread takes the same barriers and arrivals whatever its waits returned.
     grid_dependency_wait();  // qkv; and the partials may still be read
     grid_launch_dependents();
-    const int st = threadIdx.x - 64;
+    const int st = threadIdx.x - 32 * wide_first(k8);
     const int t = st >> 7;
     const int q4 = warp & 3;
     const int r = q4 * 32 + lane;
@@ -295,10 +347,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     constexpr int kQThreads = kShared ? 128 : 256;  // a tile's own rows, or both the same
     const int qt = kShared ? st & 127 : st;
     uint8_t* qd = qs + (kShared ? t * 32768 : 0);
-    start_queries<128, k8, kQThreads>(p, g, row0, qd, ps, qt);
+    uint8_t* stage = vs + (kShared ? t * 32768 : 0);  // 8 bits: no values there yet
+    start_queries<128, k8, kQThreads>(p, g, row0, qd, stage, qt);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(q_sent));
-    finish_queries<128, k8, kQThreads>(p, qd, ps, rf_s + (kShared ? t * 128 : 0), qt);
+    finish_queries<128, k8, kQThreads>(p, qd, stage, rf_s + (kShared ? t * 128 : 0), qt);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(q_bar));
@@ -319,8 +372,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     const uint32_t s_at = tmem + lane_addr + static_cast<uint32_t>(t * 128);
     const uint32_t o_at = tmem + lane_addr + 256u + static_cast<uint32_t>(t * 128);
-    uint8_t* pt = ps + t * Sh::kPBytes + r * 128;
-    const int sw = r & 7;
     for (int k = 0; k < mine; ++k) {
       const int left = p.past - key_of(k);  // keys from this block on
       const float* ks = nullptr;            // this block's key scales, value scales, log2 of them
@@ -370,14 +421,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // The block's halves of 64 keys in turn: weights with the running m, their sum
       // and (8 bits) the largest product with a value scale.  If the sum (the product)
       // has left its range, m is raised and the half done again; its scores are still
-      // there, for bf16 weights wait in registers until they are known to be good.
+      // there, for the weights wait in registers until they are known to be good.
       // The first half's value product runs under the second half's exponentials.
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int base = half * 64;
         float2 acc;
         float top;
-        uint32_t pk[k8 ? 1 : 32];
+        uint32_t pk[32];
         auto weights32 = [&](const uint32_t (&sv)[32], int c, bool tail) {  // keys base + c ...
           float2 e[16];
           scaled(sv, base + c, m, tail, e);
@@ -388,19 +439,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if constexpr (k8) {
               e[j] = mul2(e[j], *reinterpret_cast<const float2*>(ks + 128 + base + c + 2 * j));
               top = fmaxf(top, fmaxf(e[j].x, e[j].y));
+              const __half2 h = __float22half2_rn(e[j]);
+              pk[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
             } else {
               pk[c / 2 + j] = pack_bf16x2(e[j].x, e[j].y);
-            }
-          }
-          if constexpr (k8) {  // rows of 128 bytes, 16-byte piece j at j ^ (r % 8), in 3 parts
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint4 a4, b4, c4;
-              split_weights(e + 8 * h, a4, b4, c4);
-              uint8_t* at = pt + ((((base + c) / 16 + h) ^ sw) << 4);
-              *reinterpret_cast<uint4*>(at) = a4;
-              *reinterpret_cast<uint4*>(at + 16384) = b4;
-              *reinterpret_cast<uint4*>(at + 32768) = c4;
             }
           }
         };
@@ -472,16 +514,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (raised || !__any_sync(0xffffffffu, need)) break;
         }
         l += acc.x + acc.y;
-        if constexpr (k8) {
-          fence_proxy_async_smem();  // the weights are read by the MMA through the async proxy
-        } else {
-          // two keys a column, over scores that have been read
+        // two keys a column, over scores that have been read
 #pragma unroll
-          for (int j = 0; j < 32; j += 16)
-            tmem_st16(s_at + static_cast<uint32_t>(half * 32 + j),
-                      *reinterpret_cast<const uint32_t(*)[16]>(pk + j));
-          tmem_wait_st();
-        }
+        for (int j = 0; j < 32; j += 16)
+          tmem_st16(s_at + static_cast<uint32_t>(half * 32 + j),
+                    *reinterpret_cast<const uint32_t(*)[16]>(pk + j));
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * t + half]));
@@ -504,9 +542,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       *reinterpret_cast<float2*>(p.part_ml + out_row * 2) =
           make_float2(m + static_cast<float>(shift), l * down);
     // O row by row: a warp turns 64 columns of its 32 rows at a time through 8 KB
-    // of P_t, or of the ring, which is empty by now (16-byte piece c of row r at c ^ (r % 16)), so that 16 lanes
+    // of the ring, which is empty by now (16-byte piece c of row r at c ^ (r % 16)), so that 16 lanes
     // write 256 contiguous bytes
-    uint8_t* turn = (k8 ? ps + t * Sh::kPBytes : ring + t * 32768) + q4 * 8192;
+    uint8_t* turn = ring + t * 32768 + q4 * 8192;
     float4* po = reinterpret_cast<float4*>(p.part_o + (out_row - lane) * kAttnHeadDim);
     const bool have = ok && mine > 0;  // unwritten TMEM may hold anything
 #pragma unroll 1

@@ -112,7 +112,7 @@ PairKernel pair_kernel_for(int epi, bool a_mn, bool b_mn) {
 
 // The tree-attention kernels' instantiations for a bf16 and for an 8-bit cache:
 // 16, 32 or 64 query rows per block, then the wide kernel's 128 rows (the key
-// blocks split between its two tiles) and, bf16, 256 (shared by them).
+// blocks split between its two tiles) and 256 (shared by them).
 using TreeKernel = void (*)(const CUtensorMap, const CUtensorMap, const tpb::TreeParams);
 struct TreeLaunch {
   TreeKernel kernel;
@@ -128,21 +128,21 @@ constexpr TreeLaunch tree_launch() {
 template <bool k8, bool kShared>
 constexpr TreeLaunch wide_launch() {
   using Sh = tpb::WideShape<k8, kShared>;
-  return TreeLaunch{tpb::attn_tree_wide_kernel<k8, kShared>, Sh::kTileRows, tpb::kWideThreads,
-                    Sh::kSmem, 1, kShared ? 1 : 2};
+  return TreeLaunch{tpb::attn_tree_wide_kernel<k8, kShared>, Sh::kTileRows,
+                    tpb::wide_threads(k8), Sh::kSmem, 1, kShared ? 1 : 2};
 }
 const TreeLaunch kTreeLaunches[] = {
     tree_launch<16, false>(), tree_launch<32, false>(), tree_launch<64, false>(),
     wide_launch<false, false>(), wide_launch<false, true>()};
-const TreeLaunch kTreeLaunchesKv8[] = {tree_launch<16, true>(), tree_launch<32, true>(),
-                                       tree_launch<64, true>(), wide_launch<true, false>()};
+const TreeLaunch kTreeLaunchesKv8[] = {
+    tree_launch<16, true>(), tree_launch<32, true>(), tree_launch<64, true>(),
+    wide_launch<true, false>(), wide_launch<true, true>()};
 
 // The instantiation for `rows` query rows per key-value head: the smallest that
 // holds them, so that the cache is read once; the largest above that.
 const TreeLaunch& tree_launch_for(int rows, bool k8) {
-  if (rows <= 64) return (k8 ? kTreeLaunchesKv8 : kTreeLaunches)[rows <= 16 ? 0 : rows <= 32 ? 1 : 2];
-  if (k8) return kTreeLaunchesKv8[3];
-  return kTreeLaunches[rows <= 128 ? 3 : 4];
+  const int which = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 3 : 4;
+  return (k8 ? kTreeLaunchesKv8 : kTreeLaunches)[which];
 }
 
 bool tree_attrs(const TreeLaunch& l) {
