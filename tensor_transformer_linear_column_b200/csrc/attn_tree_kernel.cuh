@@ -247,7 +247,8 @@ __device__ __forceinline__ void start_queries(const TreeParams& p, int g, int ro
                                               uint8_t* stage, int st) {
   const int l = st & 15;
 #pragma unroll 1
-  for (int r = st >> 4; r < kRows; r += kThreads >> 4) {
+  for (int i = 0; i < kRows * 16 / kThreads; ++i) {
+    const int r = (st >> 4) + i * (kThreads >> 4);
     const bool in = row0 + r < p.R;
     const int rr = in ? row0 + r : 0;
     const int tok = p.G == 1 ? rr : static_cast<int>(__umulhi(static_cast<unsigned>(rr), p.g_magic));
@@ -269,7 +270,8 @@ __device__ __forceinline__ void finish_queries(const TreeParams& p, uint8_t* qs,
   if constexpr (k8) {
     const int l = st & 15;
 #pragma unroll 1
-    for (int r = st >> 4; r < kRows; r += kThreads >> 4) {
+    for (int i = 0; i < kRows * 16 / kThreads; ++i) {
+      const int r = (st >> 4) + i * (kThreads >> 4);
       float x[8];
       unpack8(*reinterpret_cast<const uint4*>(stage + r * 256 + l * 16), x);
       float amax = abs_max8(x);
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = warp_index();
   const int lane = threadIdx.x & 31;
   const int chunk = blockIdx.x;
   const int g = blockIdx.y;
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     grid_dependency_wait();  // qkv; and the partials may still be read
     grid_launch_dependents();
     const int st = threadIdx.x - 64;
-    const int wg = st >> 7;
+    const int wg = (warp - 2) >> 2;
     const int et = st & 127;
     const int q4 = warp & 3;
     const int r = q4 * 32 + lane;
@@ -890,7 +892,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     attn_tree_merge_kernel(const TreeMergeParams p) {
   __shared__ float4 red_o[kMergeWarps][32];
   __shared__ float red_l[kMergeWarps], red_m[kMergeWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int w = warp & (p.warps - 1);
   const int wid = (blockIdx.x * kMergeWarps + warp) / p.warps;
   MergeState st{neg_inf(), 0.0f, 0.0f, make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -943,7 +945,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
         const int upto = i - word * 64 + 1;                   // tokens j <= i
         bits &= upto >= 64 ? ~0ull : upto > 0 ? (1ull << upto) - 1ull : 0ull;
       }
-      bits &= mine;
+      bits = __shfl_sync(0xffffffffu, bits & mine, 0);  // the same in all lanes, and known to be
       while (bits != 0ull) {
         uint2 kr[kMergeTokens], vr[kMergeTokens];
         float s[kMergeTokens], ks = 1.0f, vs = 1.0f;

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(final_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = warp_index();
   const int lane = threadIdx.x & 31;
   const int chunk = blockIdx.x;
   const int g = blockIdx.y;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
     grid_dependency_wait();  // qkv; and the partials may still be read
     grid_launch_dependents();
     const int st = threadIdx.x - 32 * wide_first(k8);
-    const int t = st >> 7;
+    const int t = (warp - wide_first(k8)) >> 2;
     const int q4 = warp & 3;
     const int r = q4 * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(q4 * 32) << 16;

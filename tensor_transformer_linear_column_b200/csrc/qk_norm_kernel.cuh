@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_kernel(const QkPar
   __shared__ __align__(8) uint64_t done_bar[kQkStages];   // the computing warps are done with both
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   constexpr int kPerWarp = 32 / kLanes;         // heads a warp holds at once
   constexpr int kStep = kQkWarps * kPerWarp;    // heads a block holds at once
   const QkLane q = qk_lane<kPairs>(lane % kLanes, p.d, p.rot);

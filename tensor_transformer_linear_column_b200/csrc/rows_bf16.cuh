@@ -35,6 +35,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&r);
 }
 
+// This warp's index in the block, known to be the same in all its lanes: where loops
+// and branches depend on threadIdx directly, the compiler reconverges the warp
+// around every shuffle in them (300 cycles each).
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+}
+
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
