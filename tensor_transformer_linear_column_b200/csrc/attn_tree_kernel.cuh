@@ -232,7 +232,8 @@ __device__ __forceinline__ uint32_t half2_of_e4m3x2(uint32_t codes) {
 // operand, by kThreads threads (16 lanes a row): bf16 as two 64-wide halves, or
 // the 8-bit hi / lo parts with each row's factor in rf_s.  Rows at or past R are
 // zero.  The first call starts the copies (16 bytes a thread each; 8 bits: raw,
-// into `stage`), the second waits for this thread's and splits them.  The ring's
+// into `stage`), the second waits for this thread's and splits them, four rows at a
+// time.  The ring's
 // loads start after the first call: behind them these few KB would land 6,000
 // cycles later.  Rolled loops: a block runs them once, and each instruction line it
 // has to fetch costs more than the loop.
@@ -269,7 +270,7 @@ __device__ __forceinline__ void finish_queries(const TreeParams& p, uint8_t* qs,
   asm volatile("cp.async.wait_all;" ::: "memory");
   if constexpr (k8) {
     const int l = st & 15;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < kRows * 16 / kThreads; ++i) {
       const int r = (st >> 4) + i * (kThreads >> 4);
       float x[8];

@@ -47,7 +47,7 @@ __host__ __device__ constexpr int wide_threads(bool k8) { return 32 * wide_first
 constexpr int kWideMaxStages = 10;
 constexpr float kWideSumMax = 1048576.0f;       // bf16: 64 keys' sum of weights up to 2^20
 constexpr float kWideProductMax = 60000.0f;     // 8 bits: products are fp16
-constexpr float kWideProductLog2 = 5.0f;        // a raise leaves products up to 2^5
+constexpr float kWideProductLog2 = 2.0f;        // a raise leaves products up to 2^2
 constexpr float kWideSumMaxKv8 = 1.2676506e30f; // 2^100
 
 template <bool k8, bool kShared>
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
                 }
               }
             }
-            // 8 bits: products up to 2^5, and no weight above 2^60
+            // 8 bits: products up to 2^2, and no weight above 2^60
             float mn = k8 ? fmaxf(product - kWideProductLog2, high - 60.0f) : high;
             mn = need ? fmaxf(m, mn) : m;
             // in two steps: an 8-bit row's m may rise by more than fp32's exponents
@@ -549,24 +549,22 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
     const bool have = ok && mine > 0;  // unwritten TMEM may hold anything
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-      for (int c = 0; c < 64; c += 16) {
-        uint32_t o[16];
-        if (have) {
-          tmem_ld16(o_at + static_cast<uint32_t>(half * 64 + c), o);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(turn + lane * 256 + (((c / 4 + j) ^ (lane & 15)) << 4)) =
-              have ? make_float4(__uint_as_float(o[4 * j]) * down,
-                                 __uint_as_float(o[4 * j + 1]) * down,
-                                 __uint_as_float(o[4 * j + 2]) * down,
-                                 __uint_as_float(o[4 * j + 3]) * down)
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      uint32_t o[64];
+      if (have) {
+        tmem_ld32(o_at + static_cast<uint32_t>(half * 64), *reinterpret_cast<uint32_t(*)[32]>(o));
+        tmem_ld32(o_at + static_cast<uint32_t>(half * 64 + 32),
+                  *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+        tmem_wait_ld();
       }
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        *reinterpret_cast<float4*>(turn + lane * 256 + ((j ^ (lane & 15)) << 4)) =
+            have ? make_float4(__uint_as_float(o[4 * j]) * down, __uint_as_float(o[4 * j + 1]) * down,
+                               __uint_as_float(o[4 * j + 2]) * down,
+                               __uint_as_float(o[4 * j + 3]) * down)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
       __syncwarp();
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < 32; i += 2) {
         const int rl = i + (lane >> 4), piece = lane & 15;
         const float4 v = *reinterpret_cast<const float4*>(turn + rl * 256 + ((piece ^ (rl & 15)) << 4));
