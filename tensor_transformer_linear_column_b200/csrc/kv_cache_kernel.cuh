@@ -21,7 +21,7 @@ namespace tpb {
 
 constexpr float kE4m3Max = 448.0f;
 constexpr int kCacheThreads = 256;
-constexpr int kAppendBatch = 4;  // rows a lane group takes
+constexpr int kAppendBatch = 4;  // rows a lane group takes where there are many
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -52,30 +52,30 @@ struct KvAppendParams {
   void* cache[2];       // K, V: bf16 or codes [nkv, max_len, d]
   float* scale[2];      // [nkv, max_len] (8 bits)
   int T, n, past, max_len, nq, nkv, d;
-  int lanes;            // lanes per row: the power of two >= d / 8
 };
 
 // blockIdx.y = K or V of one head (2 g + which); the block's rows are
 // consecutive cache rows, so codes and scales are written in whole lines.
 // A row index outside [0, T) leaves its cache row as it was.
-template <bool k8>
+// kLanes lanes per row: the power of two >= d / 8; kBatch rows a lane group.
+template <bool k8, int kLanes, int kBatch>
 __global__ void __launch_bounds__(kCacheThreads) kv_append_rows_kernel(const KvAppendParams p) {
   grid_dependency_wait();  // qkv comes from the preceding kernel
   grid_launch_dependents();
-  const int lane_in = threadIdx.x % p.lanes;
+  const int lane_in = threadIdx.x % kLanes;
   const int g = blockIdx.y >> 1, which = blockIdx.y & 1;
   const int e0 = lane_in * 8;
   const bool active = e0 < p.d;
-  const int per_block = kCacheThreads / p.lanes;
-  const int mine = threadIdx.x / p.lanes;
-  // a block takes kAppendBatch rows per lane group, every load issued before the
-  // first use: one row at a time took 12.5 us for 4096 tokens of 8 + 8 heads of
-  // 128 in 8 bits, now 8.9
-  const int first = blockIdx.x * per_block * kAppendBatch + mine;
-  uint4 raw[kAppendBatch];
-  bool in[kAppendBatch];
+  constexpr int per_block = kCacheThreads / kLanes;
+  const int mine = threadIdx.x / kLanes;
+  // every load is issued before the first use.  With many rows a lane group takes
+  // four: one each took 12.5 us for 4096 tokens of 8 + 8 heads of 128 in 8 bits, now
+  // 7.9.  With few it takes one: 21 tokens took 5.8 us with four, APPEND_SMALL_FIGURE.
+  const int first = blockIdx.x * per_block * kBatch + mine;
+  uint4 raw[kBatch];
+  bool in[kBatch];
 #pragma unroll
-  for (int b = 0; b < kAppendBatch; ++b) {
+  for (int b = 0; b < kBatch; ++b) {
     const int j = first + b * per_block;
     const int src = j < p.n ? (p.rows != nullptr ? __ldg(p.rows + j) : j) : -1;
     in[b] = active && src >= 0 && src < p.T;
@@ -86,14 +86,15 @@ __global__ void __launch_bounds__(kCacheThreads) kv_append_rows_kernel(const KvA
           e0));
   }
 #pragma unroll
-  for (int b = 0; b < kAppendBatch; ++b) {
+  for (int b = 0; b < kBatch; ++b) {
     const size_t row = static_cast<size_t>(g) * p.max_len + p.past + first + b * per_block;
     void* cache = which ? p.cache[1] : p.cache[0];
     if constexpr (k8) {
       float x[8];
       unpack8(raw[b], x);
       float amax = abs_max8(x);
-      for (int o = p.lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int o = kLanes >> 1; o > 0; o >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       float scale;
       const uint2 codes = kv8_codes(x, amax, scale);

@@ -850,6 +850,8 @@ cudaLaunchConfig_t launch_config(dim3 grid, int threads, int smem, cudaStream_t 
   return cfg;
 }
 
+constexpr int kTreeSms = 148;  // plans are functions of the sizes only, as plan_attn's
+
 tp_status check_append(const tp_bf16* qkv, const int* rows, const void* k, const void* v, int T,
                        int n, int past, int max_len, int nq, int nkv, int d, int t) {
   if (qkv == nullptr || k == nullptr || v == nullptr) return TP_ERR_NULL;
@@ -861,24 +863,38 @@ tp_status check_append(const tp_bf16* qkv, const int* rows, const void* k, const
   return TP_OK;
 }
 
+using AppendKernel = void (*)(const tpb::KvAppendParams);
+template <bool k8, int kBatch>
+AppendKernel append_kernel(int lanes) {
+  switch (lanes) {
+    case 2: return tpb::kv_append_rows_kernel<k8, 2, kBatch>;
+    case 4: return tpb::kv_append_rows_kernel<k8, 4, kBatch>;
+    case 8: return tpb::kv_append_rows_kernel<k8, 8, kBatch>;
+    case 16: return tpb::kv_append_rows_kernel<k8, 16, kBatch>;
+    default: return tpb::kv_append_rows_kernel<k8, 32, kBatch>;
+  }
+}
+
 template <bool k8>
 tp_status launch_append(const tpb::KvAppendParams& p, cudaStream_t stream) {
-  const int per_block = tpb::kCacheThreads / p.lanes;
-  const int rows = per_block * tpb::kAppendBatch;
+  const int lanes = row_lanes(p.d);
+  int rows = tpb::kCacheThreads / lanes;  // of a block
+  // four rows a lane group once one each would fill every SM twice over
+  const bool many = static_cast<long long>(p.n) * 2 * p.nkv > 16ll * kTreeSms * rows;
+  const AppendKernel kernel =
+      many ? append_kernel<k8, tpb::kAppendBatch>(lanes) : append_kernel<k8, 1>(lanes);
+  if (many) rows *= tpb::kAppendBatch;
   const int blocks = p.n / rows + (p.n % rows != 0 ? 1 : 0);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = launch_config(
       dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(2 * p.nkv), 1), tpb::kCacheThreads,
       0, stream, attr);
-  return cuda_ok(cudaLaunchKernelEx(&cfg, tpb::kv_append_rows_kernel<k8>, p),
-                 "launch kv_append_rows_kernel")
-             ? TP_OK
-             : TP_ERR_CUDA;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, p), "launch kv_append_rows_kernel") ? TP_OK
+                                                                                      : TP_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ attention of a few new tokens
 
-constexpr int kTreeSms = 148;  // the plan is a function of the sizes only, as plan_attn's
 
 // Chunks per head: the fewest key blocks on the busiest SM, counting three for a
 // block's set-up and partial.
@@ -975,7 +991,6 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
     a.nq = nq;
     a.nkv = nkv;
     a.d = d;
-    a.lanes = row_lanes(d);
     const tp_status s = launch_append<k8>(a, stream);
     if (s != TP_OK) return s;
   }
@@ -1486,7 +1501,6 @@ tp_status tp_kv_append(const tp_bf16* qkv, const int32_t* rows, tp_bf16* k_cache
   p.nq = n_q_heads;
   p.nkv = n_kv_heads;
   p.d = head_dim;
-  p.lanes = row_lanes(head_dim);
   return launch_append<false>(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -1513,7 +1527,6 @@ tp_status tp_kv8_append(const tp_bf16* qkv, const int32_t* rows, uint8_t* k_cach
   p.nq = n_q_heads;
   p.nkv = n_kv_heads;
   p.d = head_dim;
-  p.lanes = row_lanes(head_dim);
   return launch_append<true>(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
