@@ -420,11 +420,11 @@ size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_hea
  * sees nothing (past = 0, no bit set) is zero.  The key and value of a new
  * token reach only the rows that see it, NaN and infinities included.
  * Arithmetic: bf16 q, k, v; scores, maxima and sums in fp32; over the cached
- * keys the softmax weights are rounded to bf16 for the weighted sum of v (fp32
- * accumulate) and lie in [0, 2^4] before normalisation (the running maximum is
- * raised only when a block of 128 keys exceeds it by more than that), over the
- * new ones they stay fp32.  Every order is fixed: results are bit-identical
- * from run to run.
+ * keys the softmax weights, relative to a running maximum that is raised only
+ * when they would grow past 2^16 (or 64 keys' sum past 2^20), are rounded to bf16
+ * for the weighted sum of v (fp32 accumulate), over the new ones they stay fp32.
+ * Every order is fixed: results are bit-identical from run to run.  Finite values
+ * of magnitude up to 2^96 keep the fp32 sums finite.
  *   qkv       [T, (nq + 2 nkv) d]; tree_mask [T, ceil(T / 64)] words or NULL
  *   k_cache, v_cache [nkv, max_len, d]: rows [0, past) are read, rows
  *             [past, past + T) written
@@ -447,11 +447,14 @@ tp_status tp_attn_tree(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,
  * written as codes and scales, and what is attended to is scale * code, the
  * new tokens' own included.  The codes meet the tensor cores as they are:
  * queries are split into two E4M3 terms (exact for elements of at least 2^-9
- * of their head's largest, within 2^-17 of the largest below that), softmax
- * weights times the values' scales into three E5M2 terms (relative error
- * 2^-9, or 2^-28 of the largest weight times the largest value scale of a
- * chunk of the cache).  A query head that holds an infinity gives NaN.  Other
- * arguments, checks and errors as tp_attn_tree.
+ * of their head's largest, within 2^-17 of the largest below that).  Up to 64
+ * query rows per key-value head (T nq / nkv), softmax weights times the values'
+ * scales are split into three E5M2 terms (relative error 2^-9, or 2^-22 of the
+ * largest weight times the largest value scale of a chunk of the cache); above
+ * that the value codes are converted to fp16 and the weights times the scales are
+ * fp16 (2^-11, or 2^-27 of the largest product of a chunk).  A query head that
+ * holds an infinity gives NaN.  Other arguments, checks and errors as
+ * tp_attn_tree.
  */
 tp_status tp_attn_decode_kv8(const tp_bf16* qkv, uint8_t* k_cache, float* k_scale, uint8_t* v_cache,
                              float* v_scale, const uint64_t* tree_mask, int T, int past,

@@ -18,19 +18,22 @@
 //                               tile's scores are ready only when its weights are
 //                               free again, so one wait covers both
 //   softmax                     p = 2^(t - m) straight from the scores with the
-//                               running m; only if a sum passes 2^20 (or an 8-bit
-//                               weight the range of its terms) is m raised and the
-//                               block done again
+//                               running m, 64 keys at a time; only if their sum
+//                               passes 2^20 (8 bits: a product with a value scale
+//                               leaves fp16) is m raised and the half done again
 //   O_t += P_t V_b              tcgen05.mma, V read MN-major as it lies
 // A tile waits for its own two products, and the other tile's exponentials fill
-// that time.  Issuing a unit's scores before the value product of the tile's last
-// one (scores read early, weights held in registers until P_t is free) was slower:
-// WIDE_EARLY_FIGURES
+// that time.  64 tokens of 64 / 8 heads over 65536 cached tokens (512 rows per head):
+// 139 us, 990 TFLOP/s; 4,100 cycles for 256 rows of a key block, of which the softmax
+// of a tile takes 2,300 and its products 1,600.  On the way: keys as M and weights
+// through shared memory 312 us; rows as M 180; bf16 weights over the scores in
+// tensor memory instead of in shared memory, the ring twice as deep 177; the issuing
+// warp converged 158; weights handed over by halves 139.
 // 8-bit caches: scores as in attn_tree_kernel (queries in two E4M3 parts against
 // the codes); here two more warps turn each block's value codes into fp16 once for
 // all rows, and a row's weights times the value scales are fp16 against those
-// (relative error 2^-11; splitting them into three E5M2 terms, as for few rows, costs
-// three of eight instructions an element: 266 us instead of KV8_FIGURE for 64
+// (relative error 2^-11, or 2^-27 of the largest product; splitting them into three E5M2 terms, as for few rows, costs
+// three of eight instructions an element: 266 us instead of 184 for 64
 // tokens over 65536 rows).  A row's m bounds the products p * scale themselves, so a
 // key of a large value scale and a small weight costs the others nothing.
 #pragma once
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
     // ---------------- MMA issuer: units 0 and 1's scores, then unit i's values and
     // unit i + 2's scores.  One issuer for both tiles keeps them half a period apart;
     // with one each they fell into step, and 64 tokens over 65536 rows took 205 us
-    // instead of ISSUER_FIGURE.
+    // instead of 158.
     const bool elected = elect_one();
     bool ok = __all_sync(0xffffffffu, wait_parity(smem_u32(q_bar), 0, abort_flag));
     tc_fence_after();

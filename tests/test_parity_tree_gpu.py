@@ -5,8 +5,8 @@ scales), so what differs is arithmetic.  Bound per element, with A = sum_j p_j
 |v_j| from the oracle:
   - the result is rounded once to bf16: 2^-8 of its value
   - a softmax weight over the cached keys is rounded to bf16 (2^-8 of it), or
-    held, times its value scale, in three E5M2 terms (2^-9 of it, 2^-28 of the
-    largest weight times the largest value scale): 2^-8 A
+    held, times its value scale, in three E5M2 terms or in fp16 (2^-9 of it, or
+    2^-22 of the largest weight times the largest value scale): 2^-8 A
   - scores are fp32 sums: 2^-17 of sum |q k| / sqrt(d) at most, and with an 8-bit
     cache the queries' two E4M3 terms are off by up to 2^-17 of the head's
     largest element.  Scores here have sum |q k| / sqrt(d) under 64, so a
@@ -154,6 +154,9 @@ def test_long_cache(eight, T):
     Case(eight, T, 20011, 16, 2, "tree", seed=T).check(T)
 
 
+WIDTHS = pytest.mark.parametrize("T", [2, 20, 50], ids=["narrow", "split", "shared"])
+
+
 @EIGHT
 @pytest.mark.parametrize("T", [1, 3, 12, 40])
 def test_scores_that_grow_along_the_cache(eight, T):
@@ -171,43 +174,88 @@ def test_scores_that_grow_along_the_cache(eight, T):
 
 
 @EIGHT
-def test_one_key_far_above_a_long_flat_rest(eight):
+@WIDTHS
+def test_one_key_far_above_a_long_flat_rest(eight, T):
     # the first key takes e^9 times the weight of each other: small weights
     # must add up
-    c = Case(eight, 2, 9000, 4, 1, "causal", seed=1, q_size=1.0)
-    q = torch.zeros(2, 6, D)
+    c = Case(eight, T, 9000, 4, 1, "causal", seed=1, q_size=1.0)
+    q = torch.zeros(T, 6, D)
     q[:, :4, 0] = 4.0
-    q[:, 4:] = 0.5 * torch.randn(2, 2, D, generator=torch.Generator().manual_seed(2))
-    c.qkv = q.to(torch.bfloat16).reshape(2, -1)
-    k = 0.01 * torch.randn(1, 9005, D, generator=torch.Generator().manual_seed(3))
+    q[:, 4:] = 0.5 * torch.randn(T, 2, D, generator=torch.Generator().manual_seed(2))
+    c.qkv = q.to(torch.bfloat16).reshape(T, -1)
+    k = 0.01 * torch.randn(1, 9003 + T, D, generator=torch.Generator().manual_seed(3))
     k[0, 0, 0] = 9.0 * np.sqrt(D) / 4
-    v = 1 + 0.1 * torch.randn(1, 9005, D, generator=torch.Generator().manual_seed(4))
+    v = 1 + 0.1 * torch.randn(1, 9003 + T, D, generator=torch.Generator().manual_seed(4))
     c.set_cache(k.to(torch.bfloat16), v.to(torch.bfloat16))
     c.check()
 
 
 @EIGHT
-def test_values_of_zeros_and_of_very_different_sizes(eight):
-    c = Case(eight, 5, 700, 8, 2, "tree", seed=6)
+@WIDTHS
+def test_values_of_zeros_and_of_very_different_sizes(eight, T):
+    c = Case(eight, T, 700, 8, 2, "tree", seed=6)
     g = torch.Generator().manual_seed(7)
-    k = torch.randn(2, 708, D, generator=g)
-    v = torch.randn(2, 708, D, generator=g)
+    k = torch.randn(2, 703 + T, D, generator=g)
+    v = torch.randn(2, 703 + T, D, generator=g)
     v[0] = 0
     v[1, :300] = 0
     v[1, 300:500] *= 1e-20
     v[1, 500:] *= 1e-18
-    c.qkv.view(5, -1, D)[:, 10:] *= 0
+    c.qkv.view(T, -1, D)[:, 10:] *= 0
     c.set_cache(k.to(torch.bfloat16), v.to(torch.bfloat16))
     ctx = c.check()
-    assert (ctx.view(5, 8, D)[:, :4] == 0).all()
+    assert (ctx.view(T, 8, D)[:, :4] == 0).all()
+
+
+@WIDTHS
+def test_a_large_value_scale_under_a_small_weight_costs_the_others_little(T):
+    # one key far below the rest whose value is 2^10 times as large: the rest
+    # keeps 2^-22 of the largest weight times the largest scale
+    c = Case(True, T, 900, 4, 1, "causal", seed=2)
+    g = torch.Generator().manual_seed(5)
+    q = c.qkv.view(T, 6, D)
+    q[:, :4, 0] = 8.0
+    k = torch.randn(1, 903 + T, D, generator=g)
+    v = torch.randn(1, 903 + T, D, generator=g)
+    k[0, 5, 0] = -20.0
+    v[0, 5] *= 1024
+    c.set_cache(k.to(torch.bfloat16), v.to(torch.bfloat16))
+    c.check(T)
+
+
+@EIGHT
+@WIDTHS
+def test_infinite_and_nan_scores_in_the_cache(eight, T):
+    # a key that scores -inf takes no weight wherever it stands; one that scores
+    # NaN makes its head's rows NaN and no other's
+    c = Case(eight, T, 300, 8, 2, "causal", seed=9)
+    clean, _ = c.run()
+    bad = Case(eight, T, 300, 8, 2, "causal", seed=9)
+    if eight:
+        bad.cache[1][0, 130] = float("nan")   # the key scale
+    else:
+        bad.cache[0][0, 130] = float("nan")
+    ctx, _ = bad.run()
+    assert torch.isnan(ctx.view(T, 8, D)[:, :4]).all()
+    assert torch.equal(ctx.view(T, 8, D)[:, 4:], clean.view(T, 8, D)[:, 4:])
+    if not eight:
+        # every key of the first block scores -inf for head group 0: the others
+        # take all the weight
+        low = Case(eight, T, 300, 8, 2, "causal", seed=9)
+        low.qkv.view(T, -1, D)[:, :4, 0] = 1.0
+        low.cache[0][0, :128, 0] = -float("inf")
+        ref, mag = low.reference()
+        y = low.run()[0].double().cpu().numpy()
+        assert np.isfinite(y).all()
+        assert (np.abs(y - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -9) * mag).all()
 
 
 @EIGHT
 @pytest.mark.parametrize("past", [0, 260])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_what_is_not_finite_reaches_only_the_rows_that_see_it(eight, past, bad):
-    T = 9
-    parents = [-1, 0, 0, 1, 1, 2, -1, 6, 3]
+@pytest.mark.parametrize("T", [9, 60])
+def test_what_is_not_finite_reaches_only_the_rows_that_see_it(eight, past, bad, T):
+    parents = [-1, 0, 0, 1, 1, 2, -1, 6, 3] + [8] * (T - 9)
     c = Case(eight, T, past, 8, 2, "tree", seed=past)
     c.words = tp.tp_tree_mask(parents)
     clean, _ = c.run()
