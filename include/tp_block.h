@@ -370,8 +370,9 @@ tp_status tp_kv_append(const tp_bf16* qkv, const int32_t* rows, tp_bf16* k_cache
  * of the *_w8 calls) and one fp32 scale, and stands for scale * code:
  *   scale = max_j |x_j| / 448
  *   code_j = E4M3(x_j / scale), nearest, ties to even, at most 448 in magnitude
- * Both divisions are IEEE fp32; a row of zeros has scale 0 and zero codes.  A NaN element is not counted in the maximum
- * and becomes the NaN code; a row with an infinity reads back as NaN.
+ * Both divisions are IEEE fp32; a row of zeros has scale 0 and zero codes.  A
+ * NaN element is not counted in the maximum and becomes the NaN code; a row with
+ * an infinity reads back as NaN.
  *   k_cache, v_cache [nkv, max_len, d] bytes; k_scale, v_scale [nkv, max_len]
  */
 tp_status tp_kv8_append(const tp_bf16* qkv, const int32_t* rows, uint8_t* k_cache, float* k_scale,
@@ -423,8 +424,8 @@ size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_hea
  * keys the softmax weights, relative to a running maximum that is raised only
  * when they would grow past 2^16 (or 64 keys' sum past 2^20), are rounded to bf16
  * for the weighted sum of v (fp32 accumulate), over the new ones they stay fp32.
- * Every order is fixed: results are bit-identical from run to run.  Finite values
- * of magnitude up to 2^96 keep the fp32 sums finite.
+ * Every order is fixed: results are bit-identical from run to run.  Scores
+ * q_i,h . k_j of magnitude up to 2^96 and values up to 2^80 are in range.
  *   qkv       [T, (nq + 2 nkv) d]; tree_mask [T, ceil(T / 64)] words or NULL
  *   k_cache, v_cache [nkv, max_len, d]: rows [0, past) are read, rows
  *             [past, past + T) written

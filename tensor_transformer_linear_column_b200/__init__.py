@@ -719,18 +719,18 @@ def _tree_workspace(T: int, blocks: int, n_q_heads: int, n_kv_heads: int, head_d
 
 def _tree_call(name, qkv, cache_ptrs, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree,
                tree_mask, ctx, workspace, stream, dev) -> torch.Tensor:
-    T = qkv.shape[0]
+    T, past = qkv.shape[0], int(past)
     _expect_shape(tree_mask, "tree_mask", (T, (T + 63) // 64))
     if ctx is None:
         ctx = _empty_on(qkv, (T, n_q_heads * head_dim), stream)
     else:
         _expect_shape(ctx, "ctx", (T, n_q_heads * head_dim))
     workspace = _workspace(
-        workspace, _tree_workspace(T, (past + 127) // 128, n_q_heads, n_kv_heads, head_dim), qkv,
-        dev, stream)
+        workspace, _tree_workspace(T, (past + 127) // 128, int(n_q_heads), int(n_kv_heads),
+                                   int(head_dim)), qkv, dev, stream)
     st = getattr(load(), name)(
         _ptr(qkv, "qkv", dev), *cache_ptrs, _ptr_typed(tree_mask, "tree_mask", dev, torch.int64), T,
-        int(past), max_len, int(n_q_heads), int(n_kv_heads), int(head_dim), int(tp_degree),
+        past, max_len, int(n_q_heads), int(n_kv_heads), int(head_dim), int(tp_degree),
         _ptr(ctx, "ctx", dev), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream(stream))
     _check(st, name)

@@ -76,6 +76,9 @@ constexpr int kTreeMaxStages = 8;
 constexpr float kLazyLog2 = 16.0f;
 constexpr float kLazyLog2Kv8 = 10.0f;
 constexpr float kUnsetMax = -1e30f;     // the running maximum before the first key
+// (what a preceding kernel may have written is read with plain loads: these kernels
+// start before it ends, and the read-only path is for data that stays as it is
+// for a kernel's whole life)
 constexpr int kWeightShift = 5;         // 8 bits: weights are split after times 2^5
 
 struct TreeParams {
@@ -323,10 +326,9 @@ __device__ __forceinline__ void append_pass(const TreeParams& p, int g, int part
   const bool in = item < 2 * p.T;
   uint4 raw = make_uint4(0, 0, 0, 0);
   if (in)
-    raw = __ldg(reinterpret_cast<const uint4*>(
-                    p.qkv + (static_cast<size_t>(item >> 1) * (p.nq + 2 * p.nkv) + p.nq +
-                             (item & 1) * p.nkv + g) * kAttnHeadDim) +
-                l);
+    raw = reinterpret_cast<const uint4*>(
+        p.qkv + (static_cast<size_t>(item >> 1) * (p.nq + 2 * p.nkv) + p.nq + (item & 1) * p.nkv +
+                 g) * kAttnHeadDim)[l];
   const size_t row = static_cast<size_t>(g) * p.max_len + p.past + (item >> 1);
   void* cache = item & 1 ? p.cache[1] : p.cache[0];
   if constexpr (!k8) {
@@ -618,8 +620,8 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       scale_k = p.cache_scale[0] + static_cast<size_t>(g) * p.max_len + key0 + r;
       scale_v = p.cache_scale[1] + static_cast<size_t>(g) * p.max_len + key0 + r;
       if (key0 + r < p.past) {
-        k_next = __ldg(scale_k);
-        v_next = __ldg(scale_v);
+        k_next = *scale_k;
+        v_next = *scale_v;
       }
     }
     for (int b = 0; b < nbc; ++b) {
@@ -630,8 +632,8 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
         vscale = v_next;
         k_next = v_next = 0.0f;
         if (b + 1 < nbc && r + 128 < left) {
-          k_next = __ldg(scale_k + (b + 1) * 128);
-          v_next = __ldg(scale_v + (b + 1) * 128);
+          k_next = scale_k[(b + 1) * 128];
+          v_next = scale_v[(b + 1) * 128];
         }
       }
       ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&s_full[slot]), (b >> 1) & 1,

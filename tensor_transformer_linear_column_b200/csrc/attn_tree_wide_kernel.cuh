@@ -32,9 +32,9 @@
 // 8-bit caches: scores as in attn_tree_kernel (queries in two E4M3 parts against
 // the codes); here two more warps turn each block's value codes into fp16 once for
 // all rows, and a row's weights times the value scales are fp16 against those
-// (relative error 2^-11, or 2^-27 of the largest product; splitting them into three E5M2 terms, as for few rows, costs
-// three of eight instructions an element: 266 us instead of 184 for 64
-// tokens over 65536 rows).  A row's m bounds the products p * scale themselves, so a
+// (relative error 2^-11, or 2^-27 of the largest product; splitting them into three
+// E5M2 terms, as for few rows, costs three of eight instructions an element: 266 us
+// instead of 184 for 64 tokens over 65536 rows).  A row's m bounds the products p * scale themselves, so a
 // key of a large value scale and a small weight costs the others nothing.
 #pragma once
 
@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
     const size_t sc_row = static_cast<size_t>(g) * p.max_len + r;
     if constexpr (k8) {
       if (mine > 0 && key_of(0) + r < p.past) {
-        k_next = __ldg(p.cache_scale[0] + sc_row + key_of(0));
-        v_next = __ldg(p.cache_scale[1] + sc_row + key_of(0));
+        k_next = p.cache_scale[0][sc_row + key_of(0)];
+        v_next = p.cache_scale[1][sc_row + key_of(0)];
       }
     }
     const uint32_t s_at = tmem + lane_addr + static_cast<uint32_t>(t * 128);
@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
         ks = slot;
         k_next = v_next = 0.0f;
         if (k + 1 < mine && key_of(k + 1) + r < p.past) {
-          k_next = __ldg(p.cache_scale[0] + sc_row + key_of(k + 1));
-          v_next = __ldg(p.cache_scale[1] + sc_row + key_of(k + 1));
+          k_next = p.cache_scale[0][sc_row + key_of(k + 1)];
+          v_next = p.cache_scale[1][sc_row + key_of(k + 1)];
         }
         named_barrier_sync(1u + static_cast<uint32_t>(t), 128);
       }
@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
       *reinterpret_cast<float2*>(p.part_ml + out_row * 2) =
           make_float2(m + static_cast<float>(shift), l * down);
     // O row by row: a warp turns 64 columns of its 32 rows at a time through 8 KB
-    // of the ring, which is empty by now (16-byte piece c of row r at c ^ (r % 16)), so that 16 lanes
-    // write 256 contiguous bytes
+    // of the ring, which is empty by now (16-byte piece c of row r at c ^ (r % 16)),
+    // so that 16 lanes write 256 contiguous bytes
     uint8_t* turn = ring + t * 32768 + q4 * 8192;
     float4* po = reinterpret_cast<float4*>(p.part_o + (out_row - lane) * kAttnHeadDim);
     const bool have = ok && mine > 0;  // unwritten TMEM may hold anything

@@ -70,21 +70,22 @@ __global__ void __launch_bounds__(kCacheThreads) kv_append_rows_kernel(const KvA
   const int mine = threadIdx.x / kLanes;
   // every load is issued before the first use.  With many rows a lane group takes
   // four: one each took 12.5 us for 4096 tokens of 8 + 8 heads of 128 in 8 bits, now
-  // 7.9.  With few it takes one: 21 tokens took 5.8 us with four,
-  // 2.7 with one.
+  // 8.1 (3.1 TB/s).  With few it takes one: 21 tokens took 5.8 us with four, 2.7 with
+  // one.  Plain loads: this kernel starts before the one that wrote qkv ends, and the
+  // read-only path is for data that stays as it is for a kernel's whole life.
   const int first = blockIdx.x * per_block * kBatch + mine;
   uint4 raw[kBatch];
   bool in[kBatch];
 #pragma unroll
   for (int b = 0; b < kBatch; ++b) {
     const int j = first + b * per_block;
-    const int src = j < p.n ? (p.rows != nullptr ? __ldg(p.rows + j) : j) : -1;
+    const int src = j < p.n ? (p.rows != nullptr ? p.rows[j] : j) : -1;
     in[b] = active && src >= 0 && src < p.T;
     raw[b] = make_uint4(0, 0, 0, 0);
     if (in[b])
-      raw[b] = __ldg(reinterpret_cast<const uint4*>(
+      raw[b] = *reinterpret_cast<const uint4*>(
           p.qkv + (static_cast<size_t>(src) * (p.nq + 2 * p.nkv) + p.nq + which * p.nkv + g) * p.d +
-          e0));
+          e0);
   }
 #pragma unroll
   for (int b = 0; b < kBatch; ++b) {
@@ -119,9 +120,9 @@ struct Kv8ReadParams {
 constexpr int kReadBatch = 8;
 
 // Rows [start, start + count) of every head: blockIdx.y = 2 g + which.  A thread
-// turns 8 codes into 16 bytes at a time, so a warp's stores are whole lines
-// (16 codes into two 16-byte stores each: 75 us for 65536 rows of 8 + 8 heads of 128, now 62, as fast as a plain
-// copy of as many bytes).
+// turns 8 codes into 16 bytes at a time, so a warp's stores are whole lines: 65536
+// rows of 8 + 8 heads of 128 in 62 us (6.5 TB/s, as fast as a plain copy of as many
+// bytes); with 16 codes into two 16-byte stores each 75.
 __global__ void __launch_bounds__(kCacheThreads) kv8_read_kernel(const Kv8ReadParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -142,8 +143,8 @@ __global__ void __launch_bounds__(kCacheThreads) kv8_read_kernel(const Kv8ReadPa
   for (int b = 0; b < kReadBatch; ++b) {
     const long long i = i0 + b * kCacheThreads;
     if (i < pieces) {
-      raw[b] = __ldg(src + i);
-      s[b] = __ldg(sc + i / per_row);
+      raw[b] = src[i];
+      s[b] = sc[i / per_row];
     }
   }
 #pragma unroll

@@ -224,7 +224,7 @@ __device__ __forceinline__ void bulk_wait_all() {
 // The warps meet at mbarriers only, so loads, arithmetic and stores of different
 // tokens overlap at any number of registers, and no warp waits for a slower one
 // before the ring is used up.  4096 tokens of 64 + 8 + 8 heads of 128, out of
-// place: forward 30 us (5.5 TB/s, 86 % of a plain copy's rate), backward 53 us
+// place: forward 29 us (5.7 TB/s, 89 % of a plain copy's rate), backward 52 us
 // (4.8 TB/s; without any arithmetic 42).  With each token's loads waited for by the
 // block that computes on it 39 and 67; with a block barrier per token 30 and 59.
 // Backward, 10 and 12 computing warps a block took 61 and 65, one block of 16 per
@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_kernel(const QkPar
   } else if (warp == kQkWarps) {
     // ---------------- copies
     if (lane == 0) {
+      fence_proxy_async_global();  // qkv was written by plain stores
       int filled = 0;
       for (; filled < kQkStages - 1; ++filled) fill(filled);
       for (int k = 0; k < tokens; ++k) {
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_kernel(const QkPar
     for (int k = 0; k < tokens; ++k) {
       const int st = k % kQkStages;
       const int token = static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x);
-      const int position = p.positions != nullptr ? __ldg(p.positions + token) : p.past + token;
+      const int position = p.positions != nullptr ? p.positions[token] : p.past + token;
       if (k >= kQkStages &&
           !__all_sync(0xffffffffu, wait_parity(smem_u32(&done_bar[st]),
                                                ((k - kQkStages) / kQkStages) & 1, abort_flag)))

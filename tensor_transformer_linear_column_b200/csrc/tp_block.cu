@@ -754,7 +754,7 @@ int row_lanes(int d) { return next_pow2(d / 8); }
 
 // An element index of a cache or of qkv stays far inside 64 bits.
 bool cache_ok(int nkv, int max_len, int d) {
-  return max_len >= 1 && max_len <= INT_MAX - 256 &&
+  return max_len >= 1 && max_len <= INT_MAX - 1024 &&
          static_cast<long long>(nkv) * max_len * d <= (1ll << 40) && nkv <= 32767;
 }
 

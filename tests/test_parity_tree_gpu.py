@@ -315,6 +315,104 @@ def test_on_another_stream_and_in_graphs(eight):
         assert all(torch.equal(o, want) for o in outs)
 
 
+@EIGHT
+def test_calls_on_two_streams_at_once(eight):
+    a, b = Case(eight, 5, 9000, 16, 2, "tree", seed=1), Case(eight, 40, 9000, 16, 2, "any", seed=2)
+    want = [c.run()[0] for c in (a, b)]
+    call = tp.tp_attn_decode_kv8 if eight else tp.tp_attn_tree
+    dev = [[m.cuda() for m in c.cache] for c in (a, b)]
+    qkv, mask = [c.qkv.cuda() for c in (a, b)], [c.words.cuda() for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, c in enumerate((a, b)):
+            got[i].append(call(qkv[i], *dev[i], c.past, 16, 2, D, 1, tree_mask=mask[i],
+                               stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+@EIGHT
+@pytest.mark.parametrize("T", [3, 50])
+def test_steps_that_follow_each_other_see_what_the_last_one_wrote(eight, T):
+    # append, attend, append, attend ... without a wait in between, under each set of
+    # launch options: a kernel that starts before the last one ends must still read
+    # the rows and scales that it wrote, one row a step, all in one line of scales
+    nq, nkv, past, steps = 8, 2, 250, 9
+    g = torch.Generator().manual_seed(4)
+    new = [torch.randn(1, (nq + 2 * nkv) * D, generator=g).to(torch.bfloat16).cuda()
+           for _ in range(steps)]
+    c = Case(eight, T, past, nq, nkv, "any", seed=7, extra=steps + 3)
+    qkv, mask = c.qkv.cuda(), c.words.cuda()
+    call = tp.tp_attn_decode_kv8 if eight else tp.tp_attn_tree
+    append = tp.tp_kv8_append if eight else tp.tp_kv_append
+
+    def run(wait):
+        dev, out = [m.cuda() for m in c.cache], []
+        torch.cuda.synchronize()
+        for i, x in enumerate(new):
+            append(x, *dev, past + i, nq, nkv, D, 1)
+            if wait:
+                torch.cuda.synchronize()
+            out.append(call(qkv, *dev, past + i + 1, nq, nkv, D, 1, tree_mask=mask))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return out, dev
+
+    prev = tp.tp_get_launch_options()
+    try:
+        tp.tp_set_launch_options(0)
+        want, cache = run(True)
+        for options in (0, tp.TP_OPT_PDL, tp.TP_OPT_PDL | tp.TP_OPT_STATIC_WEIGHTS):
+            tp.tp_set_launch_options(options)
+            for _ in range(5):
+                got, other = run(False)
+                assert all(torch.equal(x, y) for x, y in zip(got, want))
+                assert all(torch.equal(x[:, :past + steps], y[:, :past + steps])
+                           for x, y in zip(other, cache))
+    finally:
+        tp.tp_set_launch_options(prev)
+
+
+@EIGHT
+@pytest.mark.parametrize("T", [2, 20, 50])
+def test_what_a_workspace_held_does_not_matter(eight, T):
+    c = Case(eight, T, 700, 8, 2, "any", seed=5)
+    want, _ = c.run()
+    need = tp.tp_attn_tree_workspace_bytes(T, 700, 8, 2, D)
+    ws = torch.full((need + 64,), 0xff, dtype=torch.uint8, device="cuda")
+    got, _ = c.run(workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert (ws[need:] == 0xff).all()
+
+
+@EIGHT
+@pytest.mark.parametrize("T", [2, 50])
+def test_offsets_past_32_bits(eight, T):
+    # the last head's rows start behind 2^32 elements; the first rows of each are used
+    nq, nkv, past = 24, 6, 400
+    n = (1 << 32) // (5 * D) + 77
+    c = Case(eight, T, past, nq, nkv, "tree", seed=8)
+    small = [m.cuda() for m in c.cache]
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of free device memory")
+    want, _ = c.run(dev=small)
+    big = []
+    for m in c.cache:
+        x = torch.empty((nkv, n) + m.shape[2:], dtype=m.dtype, device="cuda")
+        x[:, :m.shape[1]] = m.cuda()
+        big.append(x)
+    got, _ = c.run(dev=big)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for x, y in zip(big, small):
+        assert torch.equal(x[:, :past + T], y[:, :past + T])
+
+
 def test_the_tree_call_without_a_mask_is_decode():
     # the same operation as tp_attn_decode: both within their rounding of it
     c = Case(False, 4, 2000, 64, 8, "causal", seed=3)
