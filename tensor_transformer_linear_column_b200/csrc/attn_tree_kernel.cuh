@@ -919,9 +919,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     const size_t ld = static_cast<size_t>(p.nq + 2 * p.nkv) * kAttnHeadDim;
     const float4 q = cache_values<false>(
         __ldg(reinterpret_cast<const uint2*>(p.qkv + i * ld + h * kAttnHeadDim) + lane));
-    const unsigned long long mine =
-        (p.warps == 8 ? 0x0101010101010101ull : p.warps == 4 ? 0x1111111111111111ull
-         : p.warps == 2 ? 0x5555555555555555ull : ~0ull) << w;
+    const uint32_t mine =  // of 32 tokens
+        (p.warps == 8 ? 0x01010101u : p.warps == 4 ? 0x11111111u : p.warps == 2 ? 0x55555555u : ~0u)
+        << w;
     const size_t row0 = static_cast<size_t>(g) * p.max_len + p.past;
     float2 ml[kMergeChunks];
     float4 o[kMergeChunks];
@@ -945,17 +945,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     }
     // the new tokens that row i sees: bf16 from qkv, before the wait; 8 bits as
     // they were written
-    for (int word = 0; word < p.words; ++word) {
-      const int left = p.T - word * 64;                       // tokens from this word on
-      unsigned long long bits = left >= 64 ? ~0ull : (1ull << left) - 1ull;
+    for (int j0 = 0; j0 < p.T; j0 += 32) {
+      const int left = p.T - j0;  // tokens from this half word on
+      uint32_t bits = left >= 32 ? ~0u : (1u << left) - 1u;
       if (p.mask != nullptr) {
-        bits &= __ldg(p.mask + static_cast<size_t>(i) * p.words + word);
+        bits &= __ldg(reinterpret_cast<const uint32_t*>(p.mask + static_cast<size_t>(i) * p.words) +
+                      j0 / 32);
       } else {
-        const int upto = i - word * 64 + 1;                   // tokens j <= i
-        bits &= upto >= 64 ? ~0ull : upto > 0 ? (1ull << upto) - 1ull : 0ull;
+        const int upto = i - j0 + 1;  // tokens j <= i
+        bits &= upto >= 32 ? ~0u : upto > 0 ? (1u << upto) - 1u : 0u;
       }
-      bits = __shfl_sync(0xffffffffu, bits & mine, 0);  // the same in all lanes, and known to be
-      while (bits != 0ull) {
+      bits = __reduce_or_sync(0xffffffffu, bits & mine);  // the same in all lanes, and known to be
+      while (bits != 0u) {
         uint2 kr[kMergeTokens], vr[kMergeTokens];
         float s[kMergeTokens], ks = 1.0f, vs = 1.0f;
         const int slot = lane >> 3;  // the token whose score this lane will hold
@@ -963,9 +964,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
 #pragma unroll
         for (int k = 0; k < kMergeTokens; ++k) {
           kr[k] = vr[k] = make_uint2(0, 0);
-          if (bits != 0ull) {
-            const int j = word * 64 + __ffsll(static_cast<long long>(bits)) - 1;
-            bits &= bits - 1ull;
+          if (bits != 0u) {
+            const int j = j0 + __ffs(static_cast<int>(bits)) - 1;
+            bits &= bits - 1u;
             if constexpr (k8) {
               kr[k].x = __ldcg(reinterpret_cast<const unsigned int*>(
                                    p.cache[0] + (row0 + j) * kAttnHeadDim) + lane);
@@ -1057,6 +1058,248 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
   packed.y = pack_bf16x2(st.o.z * inv, st.o.w * inv);
   *(reinterpret_cast<uint2*>(p.ctx + static_cast<size_t>(i) * p.nq * kAttnHeadDim +
                              static_cast<size_t>(h) * kAttnHeadDim) + lane) = packed;
+}
+
+// The same for many rows that see every new token before them (no mask): there the
+// merge's work is the new tokens, 290 instructions for four of them and a row above.
+// Here a warp takes kHeads query heads of one token and one key-value head, which
+// see the same keys, and a block stages that head's new tokens in shared memory.  A
+// lane owns tokens for the scores (no sums across lanes) and elements 4 l .. 4 l + 3
+// for the weighted sums; the first partials are loaded meanwhile.
+// Shared memory: K and V [T][256 B] as bf16 or (8 bits) the codes as fp16, 16-byte
+// piece c of row j at c ^ (j % 8); per warp its queries in fp32 and the weights
+// [64][kHeads] of 64 tokens; 8 bits: the new rows' scales.
+constexpr int kManyWarps = 4;
+constexpr int kManyFloats = kAttnHeadDim + 64;  // of a head: its query, 64 weights
+
+template <bool k8, int kHeads>
+__global__ void __launch_bounds__(kManyWarps * 32)
+    attn_tree_merge_causal_kernel(const TreeMergeParams p) {
+  extern __shared__ __align__(16) uint8_t many_smem[];
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  uint8_t* kt = many_smem;
+  uint8_t* vt = kt + p.T * 256;
+  float* wq = reinterpret_cast<float*>(vt + p.T * 256) + warp * (kHeads * kManyFloats);
+  float* sc = reinterpret_cast<float*>(vt + p.T * 256) + kManyWarps * (kHeads * kManyFloats);
+  const int g = blockIdx.y;
+  const int parts = (p.G + kHeads - 1) / kHeads;  // of a token's heads
+  const int item = blockIdx.x * kManyWarps + warp;
+  const bool in = item < p.T * parts;
+  const int i = in ? item / parts : 0;
+  const int h0 = in ? (item - i * parts) * kHeads : 0;  // first head in the group
+  const size_t ld = static_cast<size_t>(p.nq + 2 * p.nkv) * kAttnHeadDim;
+  const int seen = in ? i + 1 : 0;  // tokens that the warp's rows see, and the block's
+  const int last = (blockIdx.x * kManyWarps + kManyWarps - 1) / parts;
+  const int limit = last + 1 < p.T ? last + 1 : p.T;
+  grid_dependency_wait();  // the partials, and in 8 bits the new rows
+  grid_launch_dependents();
+  size_t base[kHeads];
+  float2 ml[kHeads][kMergeChunks];
+  float4 po[kHeads][kMergeChunks];
+#pragma unroll
+  for (int k = 0; k < kHeads; ++k) {
+    const int rr = i * p.G + (h0 + k < p.G ? h0 + k : p.G - 1);
+    const int grp = rr / p.rows;
+    base[k] = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks * p.rows + rr - grp * p.rows;
+  }
+  auto load_chunks = [&](int c0) {
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k)
+#pragma unroll
+      for (int x = 0; x < kMergeChunks; ++x) {
+        ml[k][x] = make_float2(neg_inf(), 0.0f);
+        po[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + x < p.chunks) {
+          const size_t at = base[k] + static_cast<size_t>(c0 + x) * p.rows;
+          ml[k][x] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
+          po[k][x] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kAttnHeadDim) + lane);
+        }
+      }
+  };
+  if constexpr (k8) {
+    const size_t row0 = static_cast<size_t>(g) * p.max_len + p.past;
+    for (int x = threadIdx.x; x < limit * 16; x += kManyWarps * 32) {
+      const int j = x >> 4, c = x & 7;
+      const uint4 codes = __ldcg(reinterpret_cast<const uint4*>(
+                                     (x & 8 ? p.cache[1] : p.cache[0]) + (row0 + j) * kAttnHeadDim) + c);
+      uint8_t* at = (x & 8 ? vt : kt) + j * 256;
+      *reinterpret_cast<uint4*>(at + (((2 * c) ^ (j & 7)) << 4)) =
+          make_uint4(half2_of_e4m3x2(codes.x), half2_of_e4m3x2(codes.x >> 16),
+                     half2_of_e4m3x2(codes.y), half2_of_e4m3x2(codes.y >> 16));
+      *reinterpret_cast<uint4*>(at + (((2 * c + 1) ^ (j & 7)) << 4)) =
+          make_uint4(half2_of_e4m3x2(codes.z), half2_of_e4m3x2(codes.z >> 16),
+                     half2_of_e4m3x2(codes.w), half2_of_e4m3x2(codes.w >> 16));
+    }
+    for (int j = threadIdx.x; j < limit; j += kManyWarps * 32) {
+      sc[j] = __ldcg(p.cache_scale[0] + row0 + j);
+      sc[kTreeMaxTokens + j] = __ldcg(p.cache_scale[1] + row0 + j);
+    }
+  } else {
+    for (int x = threadIdx.x; x < limit * 32; x += kManyWarps * 32) {
+      const int j = x >> 5, c = x & 15, which = (x >> 4) & 1;
+      cp_async16(smem_u32((which ? vt : kt) + j * 256 + ((c ^ (j & 7)) << 4)),
+                 p.qkv + j * ld + (p.nq + which * p.nkv + g) * kAttnHeadDim + c * 8, true);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kHeads; ++k) {
+    const int h = h0 + k < p.G ? h0 + k : p.G - 1;
+    reinterpret_cast<float4*>(wq)[k * 32 + lane] = cache_values<false>(__ldg(
+        reinterpret_cast<const uint2*>(p.qkv + i * ld + (g * p.G + h) * kAttnHeadDim) + lane));
+  }
+  load_chunks(0);  // on their way under the new tokens' work
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+
+  auto value2 = [](uint32_t w) {  // two elements
+    if constexpr (k8)
+      return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  };
+  struct __align__(kHeads * 4) Weights {
+    float w[kHeads];
+  };
+  Weights* weights = reinterpret_cast<Weights*>(wq + kHeads * kAttnHeadDim);
+  float m[kHeads], l[kHeads];
+  float2 o[kHeads][2];
+#pragma unroll
+  for (int k = 0; k < kHeads; ++k) {
+    m[k] = neg_inf();
+    l[k] = 0.0f;
+    o[k][0] = o[k][1] = make_float2(0.0f, 0.0f);
+  }
+  const float f = p.scale * 1.4426950408889634f;
+  // 64 tokens at a time
+#pragma unroll 1
+  for (int j0 = 0; j0 < seen; j0 += 64) {
+    // scores of tokens lane and lane + 32
+    int j[2];
+    float2 acc[2][kHeads];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      j[u] = j0 + u * 32 + lane;
+      if (j[u] >= limit) j[u] = limit - 1;
+#pragma unroll
+      for (int k = 0; k < kHeads; ++k) acc[u][k] = make_float2(0.0f, 0.0f);
+    }
+#pragma unroll 2
+    for (int c = 0; c < 16; ++c) {
+      float2 kv[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 raw = *reinterpret_cast<const uint4*>(kt + j[u] * 256 + ((c ^ (j[u] & 7)) << 4));
+        kv[u][0] = value2(raw.x);
+        kv[u][1] = value2(raw.y);
+        kv[u][2] = value2(raw.z);
+        kv[u][3] = value2(raw.w);
+      }
+#pragma unroll
+      for (int k = 0; k < kHeads; ++k) {
+        const float4 qa = reinterpret_cast<const float4*>(wq)[k * 32 + 2 * c];
+        const float4 qb = reinterpret_cast<const float4*>(wq)[k * 32 + 2 * c + 1];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          acc[u][k] = fma2(kv[u][0], make_float2(qa.x, qa.y), acc[u][k]);
+          acc[u][k] = fma2(kv[u][1], make_float2(qa.z, qa.w), acc[u][k]);
+          acc[u][k] = fma2(kv[u][2], make_float2(qb.x, qb.y), acc[u][k]);
+          acc[u][k] = fma2(kv[u][3], make_float2(qb.z, qb.w), acc[u][k]);
+        }
+      }
+    }
+    // weights
+    float by[2] = {f, f}, vs[2] = {1.0f, 1.0f};
+    Weights e[2];
+    if constexpr (k8) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        by[u] *= sc[j[u]];
+        vs[u] = sc[kTreeMaxTokens + j[u]];
+      }
+    }
+    const bool see0 = j0 + lane < seen, see1 = j0 + lane + 32 < seen;
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const float s0 = see0 ? (acc[0][k].x + acc[0][k].y) * by[0] : neg_inf();
+      const float s1 = see1 ? (acc[1][k].x + acc[1][k].y) * by[1] : neg_inf();
+      float high = fmaxf(s0, s1);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, x));
+      high = fmaxf(high, m[k]);
+      const float ref = high == neg_inf() ? 0.0f : high;
+      const float a = exp2_fast(m[k] - ref);
+      const float e0 = exp2_fast(s0 - ref), e1 = exp2_fast(s1 - ref);
+      float sum = e0 + e1;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      m[k] = high;
+      l[k] = fmaf(l[k], a, sum);
+      o[k][0] = mul2(o[k][0], make_float2(a, a));
+      o[k][1] = mul2(o[k][1], make_float2(a, a));
+      e[0].w[k] = e0 * vs[0];
+      e[1].w[k] = e1 * vs[1];
+    }
+    __syncwarp();  // the last 64's have been read
+    weights[lane] = e[0];
+    weights[lane + 32] = e[1];
+    __syncwarp();
+    const int n = seen - j0 < 64 ? seen - j0 : 64;
+    for (int x0 = 0; x0 < n; x0 += 4) {
+      uint2 raw[4];
+      Weights w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int at = x0 + x < n ? x0 + x : n - 1;
+        raw[x] = *reinterpret_cast<const uint2*>(vt + (j0 + at) * 256 +
+                                                 ((lane * 8) ^ ((at & 7) << 4)));
+        w[x] = weights[at];
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (x0 + x < n) {
+          const float2 va = value2(raw[x].x), vb = value2(raw[x].y);
+#pragma unroll
+          for (int k = 0; k < kHeads; ++k) {
+            const float2 wk = make_float2(w[x].w[k], w[x].w[k]);
+            o[k][0] = fma2(wk, va, o[k][0]);
+            o[k][1] = fma2(wk, vb, o[k][1]);
+          }
+        }
+    }
+  }
+  if (!in) return;
+  for (int c0 = 0; c0 < p.chunks; c0 += kMergeChunks) {
+    if (c0 != 0) load_chunks(c0);
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      float high = m[k];
+#pragma unroll
+      for (int x = 0; x < kMergeChunks; ++x) high = fmaxf(high, ml[k][x].x);
+      const float ref = high == neg_inf() ? 0.0f : high;
+      const float a = exp2_fast(m[k] - ref);
+      m[k] = high;
+      l[k] *= a;
+      o[k][0] = mul2(o[k][0], make_float2(a, a));
+      o[k][1] = mul2(o[k][1], make_float2(a, a));
+#pragma unroll
+      for (int x = 0; x < kMergeChunks; ++x) {
+        const float e = exp2_fast(ml[k][x].x - ref);
+        l[k] = fmaf(e, ml[k][x].y, l[k]);
+        o[k][0] = fma2(make_float2(e, e), make_float2(po[k][x].x, po[k][x].y), o[k][0]);
+        o[k][1] = fma2(make_float2(e, e), make_float2(po[k][x].z, po[k][x].w), o[k][1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kHeads; ++k) {
+    if (h0 + k >= p.G) break;
+    const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];  // a row that sees nothing is zero
+    uint2 packed;
+    packed.x = pack_bf16x2(o[k][0].x * inv, o[k][0].y * inv);
+    packed.y = pack_bf16x2(o[k][1].x * inv, o[k][1].y * inv);
+    *(reinterpret_cast<uint2*>(p.ctx + static_cast<size_t>(i) * p.nq * kAttnHeadDim +
+                               static_cast<size_t>(g * p.G + h0 + k) * kAttnHeadDim) + lane) = packed;
+  }
 }
 
 }  // namespace tpb

@@ -145,6 +145,21 @@ const TreeLaunch& tree_launch_for(int rows, bool k8) {
   return (k8 ? kTreeLaunchesKv8 : kTreeLaunches)[which];
 }
 
+// The merge of many rows without a mask: query heads of a warp, of the `G` that
+// share a key-value head.
+using MergeKernel = void (*)(const tpb::TreeMergeParams);
+int merge_heads(int G) { return G >= 3 ? 4 : G; }
+template <bool k8>
+MergeKernel merge_causal_kernel(int heads) {
+  return heads == 4   ? tpb::attn_tree_merge_causal_kernel<k8, 4>
+         : heads == 2 ? tpb::attn_tree_merge_causal_kernel<k8, 2>
+                      : tpb::attn_tree_merge_causal_kernel<k8, 1>;
+}
+int merge_causal_smem(int T, int heads, bool k8) {
+  return T * 512 + tpb::kManyWarps * heads * tpb::kManyFloats * 4 +
+         (k8 ? 2 * tpb::kTreeMaxTokens * 4 : 0);
+}
+
 bool tree_attrs(const TreeLaunch& l) {
   return cuda_ok(cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, l.smem),
                  "cudaFuncSetAttribute") &&
@@ -213,6 +228,14 @@ const DeviceInfo* device_info() {
     if (!tree_attrs(l)) return nullptr;
   for (const TreeLaunch& l : kTreeLaunchesKv8)
     if (!tree_attrs(l)) return nullptr;
+  for (int heads = 1; heads <= 4; heads *= 2)
+    for (const bool k8 : {false, true})
+      if (!cuda_ok(cudaFuncSetAttribute(
+                       k8 ? merge_causal_kernel<true>(heads) : merge_causal_kernel<false>(heads),
+                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       merge_causal_smem(tpb::kTreeMaxTokens, heads, k8)),
+                   "cudaFuncSetAttribute"))
+        return nullptr;
   for (int lanes = 2; lanes <= 32; lanes *= 2)
     for (int variant = 0; variant < 4; ++variant) {
       QkKernel k = qk_kernel(lanes, variant & 1 ? TP_ROPE_PAIRS : TP_ROPE_HALF, (variant & 2) != 0);
@@ -1036,9 +1059,26 @@ tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_ca
   m.part_o = p.part_o;
   m.part_ml = p.part_ml;
   m.ctx = ctx;
+  const int rows = T * nq;
+  // Without a mask a row sees half of the new tokens: the kernel for that from where the
+  // two meet, by rows times tokens (64 / 8 heads over 1000 cached tokens: 20 new ones
+  // 13.9 us with it and 11.0 without, 32 16.9 and 17.5, 64 19.8 and 33; 32 over 8000
+  // 27.8 and 26.5; 128 of 8 / 8 heads over 1000 22.0 and 24.5).  With a mask rows
+  // usually see few.
+  if (mask == nullptr && static_cast<long long>(T) * rows > 65536) {
+    const int heads = merge_heads(p.G);
+    const int parts = (p.G + heads - 1) / heads;
+    cudaLaunchConfig_t cfg = launch_config(
+        dim3(static_cast<unsigned>((T * parts + tpb::kManyWarps - 1) / tpb::kManyWarps),
+             static_cast<unsigned>(nkv), 1),
+        tpb::kManyWarps * 32, merge_causal_smem(T, heads, k8), stream, attr);
+    return cuda_ok(cudaLaunchKernelEx(&cfg, merge_causal_kernel<k8>(heads), m),
+                   "launch attn_tree_merge_causal_kernel")
+               ? TP_OK
+               : TP_ERR_CUDA;
+  }
   // up to eight warps a row while that fills the GPU: with many rows their
   // joining costs more than it saves
-  const int rows = T * nq;
   const int items = m.chunks + (mask != nullptr ? (T < 8 ? T : 8) : (T + 1) / 2);
   m.warps = rows <= 592 ? 8 : rows <= 1184 ? 4 : rows <= 2368 ? 2 : 1;
   while (m.warps > 1 && items <= 2 * m.warps) m.warps /= 2;

@@ -154,6 +154,31 @@ def test_long_cache(eight, T):
     Case(eight, T, 20011, 16, 2, "tree", seed=T).check(T)
 
 
+@EIGHT
+@pytest.mark.parametrize("nq,nkv", [(20, 20), (20, 10), (15, 5), (20, 4), (28, 4), (64, 8), (16, 1)])
+@pytest.mark.parametrize("past,T", [(0, 128), (1, 70), (260, 66), (1025, 127), (3000, 97)])
+def test_many_causal_rows(eight, nq, nkv, past, T):
+    Case(eight, T, past, nq, nkv, "causal", seed=T + nq).check((nq, nkv, past, T))
+
+
+@EIGHT
+@pytest.mark.parametrize("past", [0, 200])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_what_is_not_finite_reaches_only_later_rows(eight, past, bad):
+    # one value element of token 66 and one key element of token 90: rows 0 .. 65 of
+    # their head as they were, and no other head's
+    T, nq, nkv = 100, 16, 4
+    c = Case(eight, T, past, nq, nkv, "causal", seed=past)
+    clean, _ = c.run()
+    c.qkv.view(T, -1, D)[66, nq + nkv + 1, 3] = bad
+    c.qkv.view(T, -1, D)[90, nq + 2, 5] = float("nan")
+    got, _ = c.run()
+    same = (got == clean).view(T, nkv, -1).all(-1).cpu()
+    assert same[:66].all() and same[:, [0, 3]].all() and same[:90, 2].all()
+    off = ~torch.isfinite(got.view(T, nkv, -1)).all(-1).cpu()
+    assert off[66:, 1].all() and off[90:, 2].all()
+
+
 WIDTHS = pytest.mark.parametrize("T", [2, 20, 50], ids=["narrow", "split", "shared"])
 
 
