@@ -145,26 +145,27 @@ def _ptr_typed(t: Optional[torch.Tensor], name: str, dev: torch.device,
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _device(t: torch.Tensor) -> torch.device:
     """The device of a call: that of its first tensor, which must be the current
     CUDA device (the library launches there; a host or other-device pointer
     handed to a kernel would fault)."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
+    dev = t.device
     cur = torch.cuda.current_device()
-    if t.device.index != cur:
-        raise ValueError(f"inputs are on {t.device} but the current device is cuda:{cur}; "
-                         f"call under torch.cuda.device({t.device.index})")
-    return t.device
+    if dev.index != cur:
+        raise ValueError(f"inputs are on {dev} but the current device is cuda:{cur}; "
+                         f"call under torch.cuda.device({dev.index})")
+    return dev
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
@@ -554,7 +555,7 @@ def tp_qk_norm_rope(qkv: torch.Tensor, past: int, n_q_heads: int, n_kv_heads: in
     gq, gk, fr, pos, rot = _qk_args(qkv, gamma_q, gamma_k, inv_freq, positions, n_q_heads,
                                     n_kv_heads, head_dim, dev)
     if out is None:
-        out = _empty_on(qkv, qkv.shape, stream)
+        out = torch.empty_like(qkv) if stream is None else _empty_on(qkv, qkv.shape, stream)
     else:
         _expect_shape(out, "out", qkv.shape)
     st = load().tp_qk_norm_rope(_ptr(qkv, "qkv", dev), gq, gk, fr, pos, qkv.shape[0], int(past),
@@ -607,18 +608,21 @@ def tp_qk_norm_rope_backward(qkv: torch.Tensor, dout: torch.Tensor, past: int, n
     return {"dqkv": dqkv, "dgamma_q": dgq, "dgamma_k": dgk}
 
 
-def _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim) -> None:
-    if qkv.dim() != 2 or qkv.shape[1] != (n_q_heads + 2 * n_kv_heads) * head_dim:
+def _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim):
+    """T and max_len."""
+    rows, shape = qkv.shape, k_cache.shape
+    if len(rows) != 2 or rows[1] != (n_q_heads + 2 * n_kv_heads) * head_dim:
         raise ValueError("qkv must be [T, (nq + 2 nkv) d]")
-    shape = k_cache.shape
     if len(shape) != 3 or shape != v_cache.shape or shape[0] != n_kv_heads or \
             shape[2] != head_dim:
         raise ValueError("caches must be [nkv, max_len, d]")
+    return rows[0], shape[1]
 
 
-def _kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev):
-    _expect_shape(k_scale, "k_scale", k_cache.shape[:2])
-    _expect_shape(v_scale, "v_scale", v_cache.shape[:2])
+def _kv8_ptrs(k_cache, k_scale, v_cache, v_scale, shape, dev):
+    """The pointers of an 8-bit cache whose scales are [nkv, max_len] = shape."""
+    _expect_shape(k_scale, "k_scale", shape)
+    _expect_shape(v_scale, "v_scale", shape)
     return (_ptr_typed(k_cache, "k_cache", dev, torch.uint8),
             _ptr_typed(k_scale, "k_scale", dev, torch.float32),
             _ptr_typed(v_cache, "v_cache", dev, torch.uint8),
@@ -640,12 +644,12 @@ def tp_kv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                  stream: Optional[torch.cuda.Stream] = None) -> None:
     """Write the keys and values of qkv's rows (int32 `rows` in that order, or all
     T) into the bf16 caches [nkv, max_len, d] from row `past` on, in place."""
-    _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    T, max_len = _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
     dev = _device(qkv)
-    rp, n = _rows(rows, qkv.shape[0], dev)
+    rp, n = _rows(rows, T, dev)
     _check(load().tp_kv_append(_ptr(qkv, "qkv", dev), rp, _ptr(k_cache, "k_cache", dev),
-                               _ptr(v_cache, "v_cache", dev), qkv.shape[0], n, int(past),
-                               k_cache.shape[1], int(n_q_heads), int(n_kv_heads), int(head_dim),
+                               _ptr(v_cache, "v_cache", dev), T, n, int(past),
+                               max_len, int(n_q_heads), int(n_kv_heads), int(head_dim),
                                int(tp_degree), _stream(stream)), "tp_kv_append")
 
 
@@ -656,12 +660,13 @@ def tp_kv8_append(qkv: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tenso
                   stream: Optional[torch.cuda.Stream] = None) -> None:
     """tp_kv_append into an 8-bit cache: E4M3 codes (uint8) [nkv, max_len, d] and
     fp32 scales [nkv, max_len], a row being scale * e4m3(code)."""
-    _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    T, max_len = _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
     dev = _device(qkv)
-    rp, n = _rows(rows, qkv.shape[0], dev)
+    rp, n = _rows(rows, T, dev)
     _check(load().tp_kv8_append(_ptr(qkv, "qkv", dev), rp,
-                                *_kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev), qkv.shape[0],
-                                n, int(past), k_cache.shape[1], int(n_q_heads), int(n_kv_heads),
+                                *_kv8_ptrs(k_cache, k_scale, v_cache, v_scale,
+                                           (n_kv_heads, max_len), dev), T,
+                                n, int(past), max_len, int(n_q_heads), int(n_kv_heads),
                                 int(head_dim), int(tp_degree), _stream(stream)), "tp_kv8_append")
 
 
@@ -685,7 +690,8 @@ def tp_kv8_read(k_cache: torch.Tensor, k_scale: torch.Tensor, v_cache: torch.Ten
     if v_out is None:
         v_out = _empty_on(k_cache, shape, stream, torch.bfloat16)
     _expect_shape(v_out, "v_out", k_out.shape)
-    _check(load().tp_kv8_read(*_kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev), int(start),
+    _check(load().tp_kv8_read(*_kv8_ptrs(k_cache, k_scale, v_cache, v_scale, (nkv, max_len), dev),
+                              int(start),
                               int(count), max_len, nkv, d, int(tp_degree),
                               _ptr(k_out, "k_out", dev), _ptr(v_out, "v_out", dev), shape[1],
                               _stream(stream)), "tp_kv8_read")
@@ -717,21 +723,27 @@ def _tree_workspace(T: int, blocks: int, n_q_heads: int, n_kv_heads: int, head_d
     return tp_attn_tree_workspace_bytes(T, 128 * blocks, n_q_heads, n_kv_heads, head_dim)
 
 
-def _tree_call(name, qkv, cache_ptrs, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree,
+def _tree_call(name, qkv, cache_ptrs, T, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree,
                tree_mask, ctx, workspace, stream, dev) -> torch.Tensor:
-    T, past = qkv.shape[0], int(past)
-    _expect_shape(tree_mask, "tree_mask", (T, (T + 63) // 64))
+    past, nq, nkv, d = int(past), int(n_q_heads), int(n_kv_heads), int(head_dim)
+    mask = None
+    if tree_mask is not None:
+        _expect_shape(tree_mask, "tree_mask", (T, (T + 63) // 64))
+        mask = _ptr_typed(tree_mask, "tree_mask", dev, torch.int64)
     if ctx is None:
-        ctx = _empty_on(qkv, (T, n_q_heads * head_dim), stream)
+        ctx = qkv.new_empty((T, nq * d)) if stream is None else _empty_on(qkv, (T, nq * d), stream)
     else:
-        _expect_shape(ctx, "ctx", (T, n_q_heads * head_dim))
-    workspace = _workspace(
-        workspace, _tree_workspace(T, (past + 127) // 128, int(n_q_heads), int(n_kv_heads),
-                                   int(head_dim)), qkv, dev, stream)
+        _expect_shape(ctx, "ctx", (T, nq * d))
+    need = _tree_workspace(T, (past + 127) // 128, nq, nkv, d)
+    if workspace is None and stream is None:
+        size = max(need, 256)
+        ws = qkv.new_empty((size + 1) // 2)
+    else:
+        ws = _workspace(workspace, need, qkv, dev, stream)
+        size = ws.numel() * ws.element_size()
     st = getattr(load(), name)(
-        _ptr(qkv, "qkv", dev), *cache_ptrs, _ptr_typed(tree_mask, "tree_mask", dev, torch.int64), T,
-        past, max_len, int(n_q_heads), int(n_kv_heads), int(head_dim), int(tp_degree),
-        _ptr(ctx, "ctx", dev), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _ptr_typed(qkv, "qkv", dev, torch.bfloat16), *cache_ptrs, mask, T, past, max_len, nq, nkv,
+        d, int(tp_degree), _ptr_typed(ctx, "ctx", dev, torch.bfloat16), ws.data_ptr(), size,
         _stream(stream))
     _check(st, name)
     return ctx
@@ -747,11 +759,11 @@ def tp_attn_tree(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     new tokens that its row of tree_mask names (int64 words on the GPU, see
     tp_tree_mask; None: causal).  Writes the new tokens' keys and values behind
     the cached ones, in place."""
-    _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    T, max_len = _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
     dev = _device(qkv)
     return _tree_call("tp_attn_tree", qkv,
                       (_ptr(k_cache, "k_cache", dev), _ptr(v_cache, "v_cache", dev)),
-                      k_cache.shape[1], past, n_q_heads, n_kv_heads, head_dim, tp_degree,
+                      T, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree,
                       tree_mask, ctx, workspace, stream, dev)
 
 
@@ -765,11 +777,11 @@ def tp_attn_decode_kv8(qkv: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.
     """tp_attn_tree over an 8-bit cache (codes uint8 [nkv, max_len, d], scales
     fp32 [nkv, max_len]); decode when tree_mask is None.  The new tokens are
     quantised as they are written, and attended to as written."""
-    _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    T, max_len = _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
     dev = _device(qkv)
     return _tree_call("tp_attn_decode_kv8", qkv,
-                      _kv8_ptrs(k_cache, k_scale, v_cache, v_scale, dev), k_cache.shape[1], past,
-                      n_q_heads, n_kv_heads, head_dim, tp_degree, tree_mask, ctx, workspace,
+                      _kv8_ptrs(k_cache, k_scale, v_cache, v_scale, (n_kv_heads, max_len), dev),
+                      T, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree, tree_mask, ctx, workspace,
                       stream, dev)
 
 
