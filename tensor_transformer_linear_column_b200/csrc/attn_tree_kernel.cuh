@@ -81,6 +81,20 @@ constexpr float kUnsetMax = -1e30f;     // the running maximum before the first 
 // for a kernel's whole life)
 constexpr int kWeightShift = 5;         // 8 bits: weights are split after times 2^5
 
+struct TreeMergeParams {
+  int T, past, nq, nkv, G, rows, chunks, max_len;
+  int words;        // mask words per token
+  int warps;        // warps per (token, query head): 1, 2, 4 or 8
+  float scale;      // 1 / sqrt(d)
+  const uint16_t* qkv;
+  const uint8_t* cache[2];         // 8 bits: the caches, for the new rows
+  const float* cache_scale[2];
+  const unsigned long long* mask;  // [T][words], or null: j <= i
+  const float* part_o;
+  const float* part_ml;
+  uint16_t* ctx;    // [T, nq d]
+};
+
 struct TreeParams {
   int T, past, nq, nkv, G;
   int R;            // query rows per key-value head: T G
@@ -90,12 +104,14 @@ struct TreeParams {
   int nb, chunks;   // key blocks per chunk, chunks per key-value head: grid x
   int max_len;
   int append;       // this kernel writes the new rows (else the launch before it has)
+  int join;         // the chunks of a head are a cluster and leave no partials
   float scale_log2; // log2(e) / sqrt(d)
   const uint16_t* qkv;       // [T, (nq + 2 nkv) d]
   void* cache[2];            // K, V [nkv, max_len, d]: bf16 or E4M3 codes
   float* cache_scale[2];     // [nkv, max_len] (8 bits)
   float* part_o;             // [groups][nkv][chunks][kRows][d]
   float* part_ml;            // [groups][nkv][chunks][kRows][2]
+  TreeMergeParams merge;     // where a head's blocks join their partials themselves
 };
 
 template <int kRows, bool k8>
@@ -157,7 +173,7 @@ __device__ __forceinline__ bool elect_one() {
 constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescHiPlain = (2048u >> 4) | (1u << 14);  // SBO 2048
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
-  return (saddr >> 4) | ((lbo >> 4) << 16);
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);  // (a cluster's address holds the rank)
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, one M x N x 16 (bf16) or x 32 (8 bits) step.
@@ -376,7 +392,175 @@ __device__ __forceinline__ void split_weights(const float2* w, uint4& a4, uint4&
   c4 = make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-template <int kRows, bool k8>
+constexpr int kMergeWarps = 8;
+constexpr int kMergeChunks = 4;  // partials a warp has in flight
+constexpr int kMergeTokens = 4;  // new tokens a warp has in flight
+
+// One running (maximum, sums, weighted sum) of a warp in base-2 units: lane l
+// owns elements 4 l .. 4 l + 3 of the weighted sum; `l` is the chunks' sum, the
+// same in every lane, `lt` the new tokens' (lane l: those of slot l / 8).
+struct MergeState {
+  float m, l, lt;
+  float4 o;
+};
+
+// Raise the maximum to at least `high`; the reference to take exponents over (0
+// while nothing finite has been seen).
+__device__ __forceinline__ float merge_raise(MergeState& a, float high) {
+  const float mn = fmaxf(a.m, high);
+  const float ref = mn == neg_inf() ? 0.0f : mn;
+  const float s = exp2_fast(a.m - ref);
+  a.o.x *= s;
+  a.o.y *= s;
+  a.o.z *= s;
+  a.o.w *= s;
+  a.l *= s;
+  a.lt *= s;
+  a.m = mn;
+  return ref;
+}
+
+__device__ __forceinline__ void merge_add(MergeState& a, float w, const float4& v) {
+  a.o.x = fmaf(w, v.x, a.o.x);
+  a.o.y = fmaf(w, v.y, a.o.y);
+  a.o.z = fmaf(w, v.z, a.o.z);
+  a.o.w = fmaf(w, v.w, a.o.w);
+}
+
+// Four elements of a row.
+template <bool k8>
+__device__ __forceinline__ float4 cache_values(const uint2& raw) {
+  if constexpr (k8) {
+    const __half2 a(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(raw.x), __NV_E4M3));
+    const __half2 b(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(raw.x >> 16), __NV_E4M3));
+    const float2 fa = __half22float2(a), fb = __half22float2(b);
+    return make_float4(fa.x, fa.y, fb.x, fb.y);
+  } else {
+    return make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
+                       __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u));
+  }
+}
+
+// The new tokens that token i sees, of those in `mine` (of every 32), for its query
+// head h of key-value head g: bf16 from qkv, 8 bits as they were written.
+template <bool k8>
+__device__ __forceinline__ void merge_tokens(MergeState& st, const TreeMergeParams& p, int i, int h,
+                                             int g, uint32_t mine, int lane) {
+  const float f = p.scale * 1.4426950408889634f;
+  const size_t ld = static_cast<size_t>(p.nq + 2 * p.nkv) * kAttnHeadDim;
+  const float4 q = cache_values<false>(
+      reinterpret_cast<const uint2*>(p.qkv + i * ld + h * kAttnHeadDim)[lane]);
+  const size_t row0 = static_cast<size_t>(g) * p.max_len + p.past;
+  for (int j0 = 0; j0 < p.T; j0 += 32) {
+    const int left = p.T - j0;  // tokens from this half word on
+    uint32_t bits = left >= 32 ? ~0u : (1u << left) - 1u;
+    if (p.mask != nullptr) {
+      bits &= reinterpret_cast<const uint32_t*>(p.mask + static_cast<size_t>(i) * p.words)[j0 / 32];
+    } else {
+      const int upto = i - j0 + 1;  // tokens j <= i
+      bits &= upto >= 32 ? ~0u : upto > 0 ? (1u << upto) - 1u : 0u;
+    }
+    bits = __reduce_or_sync(0xffffffffu, bits & mine);  // the same in all lanes, and known to be
+    while (bits != 0u) {
+      uint2 kr[kMergeTokens], vr[kMergeTokens];
+      float s[kMergeTokens], ks = 1.0f, vs = 1.0f;
+      const int slot = lane >> 3;  // the token whose score this lane will hold
+      int count = 0;
+#pragma unroll
+      for (int k = 0; k < kMergeTokens; ++k) {
+        kr[k] = vr[k] = make_uint2(0, 0);
+        if (bits != 0u) {
+          const int j = j0 + __ffs(static_cast<int>(bits)) - 1;
+          bits &= bits - 1u;
+          if constexpr (k8) {
+            kr[k].x = __ldcg(reinterpret_cast<const unsigned int*>(
+                                 p.cache[0] + (row0 + j) * kAttnHeadDim) + lane);
+            vr[k].x = __ldcg(reinterpret_cast<const unsigned int*>(
+                                 p.cache[1] + (row0 + j) * kAttnHeadDim) + lane);
+          } else {
+            const uint16_t* at = p.qkv + j * ld + (p.nq + g) * kAttnHeadDim;
+            kr[k] = reinterpret_cast<const uint2*>(at)[lane];
+            vr[k] = reinterpret_cast<const uint2*>(at + p.nkv * kAttnHeadDim)[lane];
+          }
+          if (k8 && slot == k) {
+            ks = __ldcg(p.cache_scale[0] + row0 + j);
+            vs = __ldcg(p.cache_scale[1] + row0 + j);
+          }
+          count = k + 1;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeTokens; ++k) {
+        const float4 kv = cache_values<k8>(kr[k]);
+        s[k] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, q.w * kv.w)));
+      }
+      const float dot = warp_rows_reduce<kMergeTokens, false>(s, lane);
+      const float t = slot < count ? dot * ks * f : neg_inf();
+      float high = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+      high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 16));
+      const float ref = merge_raise(st, high);
+      const float e = exp2_fast(t - ref);
+      st.lt += e;
+#pragma unroll
+      for (int k = 0; k < kMergeTokens; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, e * vs, 8 * k);
+        if (k < count) merge_add(st, wk, cache_values<k8>(vr[k]));
+      }
+    }
+  }
+}
+
+// The row's sum over the new tokens' slots, and with the chunks'.
+__device__ __forceinline__ void merge_sum(MergeState& st) {
+  st.lt += __shfl_xor_sync(0xffffffffu, st.lt, 8);
+  st.l += st.lt + __shfl_xor_sync(0xffffffffu, st.lt, 16);
+}
+
+__device__ __forceinline__ void merge_store(const MergeState& st, const TreeMergeParams& p, int i,
+                                            int h, int lane) {
+  const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;  // a row that sees nothing is zero
+  uint2 packed;
+  packed.x = pack_bf16x2(st.o.x * inv, st.o.y * inv);
+  packed.y = pack_bf16x2(st.o.z * inv, st.o.w * inv);
+  *(reinterpret_cast<uint2*>(p.ctx + static_cast<size_t>(i) * p.nq * kAttnHeadDim +
+                             static_cast<size_t>(h) * kAttnHeadDim) + lane) = packed;
+}
+
+// kMergeChunks partials (maximum, sum, weighted sum) into the state.
+__device__ __forceinline__ void merge_chunks(MergeState& st, const float2 (&ml)[kMergeChunks],
+                                             const float4 (&o)[kMergeChunks]) {
+  float high = ml[0].x;
+#pragma unroll
+  for (int k = 1; k < kMergeChunks; ++k) high = fmaxf(high, ml[k].x);
+  const float ref = merge_raise(st, high);
+#pragma unroll
+  for (int k = 0; k < kMergeChunks; ++k) {
+    const float e = exp2_fast(ml[k].x - ref);
+    st.l = fmaf(e, ml[k].y, st.l);
+    merge_add(st, e, o[k]);
+  }
+}
+
+// Shared memory of a block of the cluster.
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// kJoin: a head's chunks are one cluster, and its blocks join their partials out of
+// each other's shared memory instead of leaving them to a second launch (which in
+// 8 bits has nothing to do before this one is over: it waits for the new rows' codes).
+template <int kRows, bool k8, bool kJoin>
 __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRows, k8>::kBlocksPerSm)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
@@ -792,17 +976,20 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     }
     named_barrier_sync(bar_id, 128);
     const size_t part = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks + chunk;
+    float* part_o = kJoin ? reinterpret_cast<float*>(ring) : p.part_o + part * kRows * kAttnHeadDim;
+    float* part_ml = kJoin ? part_o + kRows * kAttnHeadDim : p.part_ml + part * kRows * 2;
+    ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[(nbc - 1) & 1]),
+                                                   ((nbc - 1) >> 1) & 1, abort_flag));
+    tc_fence_after();
+    // (kJoin: the ring is empty by now, every tile has been read)
     if (et < kCols && row0 + c0 + et < p.R) {
       const int n = c0 + et;
       float2 ml = make_float2(-nm_s[n], ((red[n] + red[kRows + n]) + red[2 * kRows + n]) +
                                           red[3 * kRows + n]);
-      *reinterpret_cast<float2*>(p.part_ml + (part * kRows + n) * 2) = ml;
+      *reinterpret_cast<float2*>(part_ml + n * 2) = ml;
     }
-    ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[(nbc - 1) & 1]),
-                                                   ((nbc - 1) >> 1) & 1, abort_flag));
-    tc_fence_after();
     const float of = k8 ? pow2i(c_exp - kWeightShift) : 1.0f;
-    float* po = p.part_o + (part * kRows + c0) * kAttnHeadDim + r;
+    float* po = part_o + c0 * kAttnHeadDim + r;
     float sum[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
@@ -826,69 +1013,36 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
     tc_fence_after();
     tmem_dealloc(tmem, static_cast<uint32_t>(Sh::kTmemCols));
   }
-}
-
-struct TreeMergeParams {
-  int T, past, nq, nkv, G, rows, chunks, max_len;
-  int words;        // mask words per token
-  int warps;        // warps per (token, query head): 1, 2, 4 or 8
-  float scale;      // 1 / sqrt(d)
-  const uint16_t* qkv;
-  const uint8_t* cache[2];         // 8 bits: the caches, for the new rows
-  const float* cache_scale[2];
-  const unsigned long long* mask;  // [T][words], or null: j <= i
-  const float* part_o;
-  const float* part_ml;
-  uint16_t* ctx;    // [T, nq d]
-};
-
-constexpr int kMergeWarps = 8;
-constexpr int kMergeChunks = 4;  // partials a warp has in flight
-constexpr int kMergeTokens = 4;  // new tokens a warp has in flight
-
-// One running (maximum, sums, weighted sum) of a warp in base-2 units: lane l
-// owns elements 4 l .. 4 l + 3 of the weighted sum; `l` is the chunks' sum, the
-// same in every lane, `lt` the new tokens' (lane l: those of slot l / 8).
-struct MergeState {
-  float m, l, lt;
-  float4 o;
-};
-
-// Raise the maximum to at least `high`; the reference to take exponents over (0
-// while nothing finite has been seen).
-__device__ __forceinline__ float merge_raise(MergeState& a, float high) {
-  const float mn = fmaxf(a.m, high);
-  const float ref = mn == neg_inf() ? 0.0f : mn;
-  const float s = exp2_fast(a.m - ref);
-  a.o.x *= s;
-  a.o.y *= s;
-  a.o.z *= s;
-  a.o.w *= s;
-  a.l *= s;
-  a.lt *= s;
-  a.m = mn;
-  return ref;
-}
-
-__device__ __forceinline__ void merge_add(MergeState& a, float w, const float4& v) {
-  a.o.x = fmaf(w, v.x, a.o.x);
-  a.o.y = fmaf(w, v.y, a.o.y);
-  a.o.z = fmaf(w, v.z, a.o.z);
-  a.o.w = fmaf(w, v.w, a.o.w);
-}
-
-// Four elements of a row.
-template <bool k8>
-__device__ __forceinline__ float4 cache_values(const uint2& raw) {
-  if constexpr (k8) {
-    const __half2 a(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(raw.x), __NV_E4M3));
-    const __half2 b(
-        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(raw.x >> 16), __NV_E4M3));
-    const float2 fa = __half22float2(a), fb = __half22float2(b);
-    return make_float4(fa.x, fa.y, fb.x, fb.y);
-  } else {
-    return make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
-                       __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u));
+  if constexpr (kJoin) {
+    __syncwarp();
+    grid_dependency_wait();  // for the warps that have not: qkv, the mask
+    cluster_sync_all();  // every block's partial, and in 8 bits the new rows
+    // one row a warp: the launch sees to it that there are enough of them
+    const int row = warp * p.chunks + chunk;
+    if (row < p.R) {
+      const int i = row / p.G, h = g * p.G + row - i * p.G;
+      MergeState st{neg_inf(), 0.0f, 0.0f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      merge_tokens<k8>(st, p.merge, i, h, g, ~0u, lane);
+      merge_sum(st);
+      float2 ml[kMergeChunks];
+      float4 o[kMergeChunks];
+      const uint32_t at_o = smem_u32(ring) + static_cast<uint32_t>(row * kAttnHeadDim + lane * 4) * 4u;
+      const uint32_t at_ml = smem_u32(ring) + static_cast<uint32_t>(kRows * kAttnHeadDim + row * 2) * 4u;
+      for (int c0 = 0; c0 < p.chunks; c0 += kMergeChunks) {
+#pragma unroll
+        for (int k = 0; k < kMergeChunks; ++k) {
+          ml[k] = make_float2(neg_inf(), 0.0f);
+          o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c0 + k < p.chunks) {
+            ml[k] = cluster_ld2(dsmem_map(at_ml, static_cast<uint32_t>(c0 + k)));
+            o[k] = cluster_ld4(dsmem_map(at_o, static_cast<uint32_t>(c0 + k)));
+          }
+        }
+        merge_chunks(st, ml, o);
+      }
+      merge_store(st, p.merge, i, h, lane);
+    }
+    cluster_sync_all();  // a block's shared memory stays until the others have read it
   }
 }
 
@@ -915,14 +1069,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     const size_t base = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks * p.rows + n;
     // qkv and the mask are complete: the preceding kernel has waited for them
     // before it let this one start
-    const float f = p.scale * 1.4426950408889634f;
-    const size_t ld = static_cast<size_t>(p.nq + 2 * p.nkv) * kAttnHeadDim;
-    const float4 q = cache_values<false>(
-        __ldg(reinterpret_cast<const uint2*>(p.qkv + i * ld + h * kAttnHeadDim) + lane));
     const uint32_t mine =  // of 32 tokens
         (p.warps == 8 ? 0x01010101u : p.warps == 4 ? 0x11111111u : p.warps == 2 ? 0x55555555u : ~0u)
         << w;
-    const size_t row0 = static_cast<size_t>(g) * p.max_len + p.past;
     float2 ml[kMergeChunks];
     float4 o[kMergeChunks];
     auto load_chunks = [&](int c0) {
@@ -943,86 +1092,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
       grid_launch_dependents();
       load_chunks(w);
     }
-    // the new tokens that row i sees: bf16 from qkv, before the wait; 8 bits as
-    // they were written
-    for (int j0 = 0; j0 < p.T; j0 += 32) {
-      const int left = p.T - j0;  // tokens from this half word on
-      uint32_t bits = left >= 32 ? ~0u : (1u << left) - 1u;
-      if (p.mask != nullptr) {
-        bits &= __ldg(reinterpret_cast<const uint32_t*>(p.mask + static_cast<size_t>(i) * p.words) +
-                      j0 / 32);
-      } else {
-        const int upto = i - j0 + 1;  // tokens j <= i
-        bits &= upto >= 32 ? ~0u : upto > 0 ? (1u << upto) - 1u : 0u;
-      }
-      bits = __reduce_or_sync(0xffffffffu, bits & mine);  // the same in all lanes, and known to be
-      while (bits != 0u) {
-        uint2 kr[kMergeTokens], vr[kMergeTokens];
-        float s[kMergeTokens], ks = 1.0f, vs = 1.0f;
-        const int slot = lane >> 3;  // the token whose score this lane will hold
-        int count = 0;
-#pragma unroll
-        for (int k = 0; k < kMergeTokens; ++k) {
-          kr[k] = vr[k] = make_uint2(0, 0);
-          if (bits != 0u) {
-            const int j = j0 + __ffs(static_cast<int>(bits)) - 1;
-            bits &= bits - 1u;
-            if constexpr (k8) {
-              kr[k].x = __ldcg(reinterpret_cast<const unsigned int*>(
-                                   p.cache[0] + (row0 + j) * kAttnHeadDim) + lane);
-              vr[k].x = __ldcg(reinterpret_cast<const unsigned int*>(
-                                   p.cache[1] + (row0 + j) * kAttnHeadDim) + lane);
-            } else {
-              const uint16_t* at = p.qkv + j * ld + (p.nq + g) * kAttnHeadDim;
-              kr[k] = __ldg(reinterpret_cast<const uint2*>(at) + lane);
-              vr[k] = __ldg(reinterpret_cast<const uint2*>(at + p.nkv * kAttnHeadDim) + lane);
-            }
-            if (k8 && slot == k) {
-              ks = __ldcg(p.cache_scale[0] + row0 + j);
-              vs = __ldcg(p.cache_scale[1] + row0 + j);
-            }
-            count = k + 1;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kMergeTokens; ++k) {
-          const float4 kv = cache_values<k8>(kr[k]);
-          s[k] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, q.w * kv.w)));
-        }
-        const float dot = warp_rows_reduce<kMergeTokens, false>(s, lane);
-        const float t = slot < count ? dot * ks * f : neg_inf();
-        float high = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 16));
-        const float ref = merge_raise(st, high);
-        const float e = exp2_fast(t - ref);
-        st.lt += e;
-#pragma unroll
-        for (int k = 0; k < kMergeTokens; ++k) {
-          const float wk = __shfl_sync(0xffffffffu, e * vs, 8 * k);
-          if (k < count) merge_add(st, wk, cache_values<k8>(vr[k]));
-        }
-      }
-    }
+    merge_tokens<k8>(st, p, i, h, g, mine, lane);
     if constexpr (!k8) {
       grid_dependency_wait();  // the partials
       grid_launch_dependents();
     }
     for (int c0 = w; c0 < p.chunks; c0 += p.warps * kMergeChunks) {
       if (!k8 || c0 != w) load_chunks(c0);
-      float high = ml[0].x;
-#pragma unroll
-      for (int k = 1; k < kMergeChunks; ++k) high = fmaxf(high, ml[k].x);
-      const float ref = merge_raise(st, high);
-#pragma unroll
-      for (int k = 0; k < kMergeChunks; ++k) {
-        const float e = exp2_fast(ml[k].x - ref);
-        st.l = fmaf(e, ml[k].y, st.l);
-        merge_add(st, e, o[k]);
-      }
+      merge_chunks(st, ml, o);
     }
-    // the new tokens' sum over their slots
-    st.lt += __shfl_xor_sync(0xffffffffu, st.lt, 8);
-    st.l += st.lt + __shfl_xor_sync(0xffffffffu, st.lt, 16);
+    merge_sum(st);
   } else {
     grid_dependency_wait();
   }
@@ -1051,13 +1130,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4)
     st.o = o;
     st.l = l;
   }
-  if (!in) return;
-  const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;  // a row that sees nothing is zero
-  uint2 packed;
-  packed.x = pack_bf16x2(st.o.x * inv, st.o.y * inv);
-  packed.y = pack_bf16x2(st.o.z * inv, st.o.w * inv);
-  *(reinterpret_cast<uint2*>(p.ctx + static_cast<size_t>(i) * p.nq * kAttnHeadDim +
-                             static_cast<size_t>(h) * kAttnHeadDim) + lane) = packed;
+  if (in) merge_store(st, p, i, h, lane);
 }
 
 // The same for many rows that see every new token before them (no mask): there the

@@ -149,6 +149,40 @@ def test_rows_whose_mask_names_nothing(eight, past, T):
 
 
 @EIGHT
+@pytest.mark.parametrize("nq,nkv", [(8, 1), (28, 4), (16, 16), (40, 40)])
+@pytest.mark.parametrize("past,T", [(129, 1), (1024, 2), (1025, 1), (1200, 4), (1537, 8), (1793, 3),
+                                    (2048, 4), (2049, 4)])
+def test_caches_around_eight_and_sixteen_blocks(eight, nq, nkv, past, T):
+    Case(eight, T, past, nq, nkv, "any", seed=past).check((nq, nkv, past, T))
+
+
+def test_short_8_bit_caches_on_two_streams_and_replayed():
+    a, b = Case(True, 4, 1500, 16, 2, "tree", seed=1), Case(True, 1, 900, 16, 2, "causal", seed=2)
+    want = [c.run()[0] for c in (a, b)]
+    dev = [[m.cuda() for m in c.cache] for c in (a, b)]
+    qkv, mask = [c.qkv.cuda() for c in (a, b)], [a.words.cuda(), None]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, c in enumerate((a, b)):
+            got[i].append(tp.tp_attn_decode_kv8(qkv[i], *dev[i], c.past, 16, 2, D, 1,
+                                                tree_mask=mask[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i]) for i in range(2) for g in got[i])
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        outs = [tp.tp_attn_decode_kv8(qkv[i], *dev[i], c.past, 16, 2, D, 1, tree_mask=mask[i])
+                for i, c in enumerate((a, b, a, b)) for i in [i % 2]]
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(outs))
+
+
+@EIGHT
 @pytest.mark.parametrize("T", [1, 4, 30])
 def test_long_cache(eight, T):
     Case(eight, T, 20011, 16, 2, "tree", seed=T).check(T)
