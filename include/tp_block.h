@@ -405,9 +405,13 @@ tp_status tp_tree_mask(const int32_t* parents, int T, uint64_t* mask);
 /*
  * Bytes of workspace that tp_attn_tree and tp_attn_decode_kv8 need for T new
  * tokens after `past` cached ones; 0 for past = 0 and for unsupported
- * arguments.  A function of the sizes only.
+ * arguments.  A function of the sizes only.  The second is what
+ * tp_attn_decode_kv8 alone needs: never more, and 0 also for a short cache whose
+ * partial results stay on chip.
  */
 size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads, int head_dim);
+size_t tp_attn_decode_kv8_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads,
+                                          int head_dim);
 
 /*
  * Attention of a tree of drafted tokens over a cache: tp_attn_decode with a
@@ -430,8 +434,9 @@ size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_hea
  *   k_cache, v_cache [nkv, max_len, d]: rows [0, past) are read, rows
  *             [past, past + T) written
  *   ctx       [T, nq d]                                            (written)
- *   workspace: at least tp_attn_tree_workspace_bytes(...) bytes, 16-byte
- *   aligned; may be NULL if that is 0; contents on return unspecified.
+ *   workspace: at least tp_attn_tree_workspace_bytes(...) bytes (or what
+ *   tp_attn_decode_kv8_workspace_bytes gives, for that call), 16-byte aligned;
+ *   may be NULL if that is 0; contents on return unspecified.
  * Requires T <= 128, head_dim == 128 and nq / nkv <= 16 (else
  * TP_ERR_UNSUPPORTED), nq a multiple of nkv, past + T <= max_len (else
  * TP_ERR_SHAPE), and t dividing both head counts.  Calls that overlap on the

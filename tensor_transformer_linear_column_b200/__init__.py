@@ -65,6 +65,7 @@ SIGNATURES = {
     "tp_kv8_read": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P]),
     "tp_tree_mask": (_I, [_P, _I, _P]),
     "tp_attn_tree_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
+    "tp_attn_decode_kv8_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
     "tp_attn_tree": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z, _P]),
     "tp_attn_decode_kv8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z,
                                 _P]),
@@ -508,7 +509,8 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor,
                dev: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
     """The caller's workspace, or one of `need` bytes (like is bf16)."""
     if workspace is None:
-        return _empty_on(like, (max(need, 256) + 1) // 2, stream)
+        size = (max(need, 256) + 1) // 2
+        return like.new_empty(size) if stream is None else _empty_on(like, size, stream)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the same device")
     return workspace
@@ -716,11 +718,19 @@ def tp_attn_tree_workspace_bytes(T: int, past: int, n_q_heads: int, n_kv_heads: 
                                                    int(n_kv_heads), int(head_dim)))
 
 
+def tp_attn_decode_kv8_workspace_bytes(T: int, past: int, n_q_heads: int, n_kv_heads: int,
+                                       head_dim: int) -> int:
+    return int(load().tp_attn_decode_kv8_workspace_bytes(int(T), int(past), int(n_q_heads),
+                                                         int(n_kv_heads), int(head_dim)))
+
+
 @functools.lru_cache(maxsize=256)
-def _tree_workspace(T: int, blocks: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
-    """The workspace for `blocks` blocks of 128 cached tokens (the size depends on
-    `past` through them alone)."""
-    return tp_attn_tree_workspace_bytes(T, 128 * blocks, n_q_heads, n_kv_heads, head_dim)
+def _tree_workspace(name: str, T: int, blocks: int, n_q_heads: int, n_kv_heads: int,
+                    head_dim: int) -> int:
+    """The workspace of a call for `blocks` blocks of 128 cached tokens (the size
+    depends on `past` through them alone)."""
+    return getattr(load(), name + "_workspace_bytes")(T, 128 * blocks, n_q_heads, n_kv_heads,
+                                                      head_dim)
 
 
 def _tree_call(name, qkv, cache_ptrs, T, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree,
@@ -734,16 +744,14 @@ def _tree_call(name, qkv, cache_ptrs, T, max_len, past, n_q_heads, n_kv_heads, h
         ctx = qkv.new_empty((T, nq * d)) if stream is None else _empty_on(qkv, (T, nq * d), stream)
     else:
         _expect_shape(ctx, "ctx", (T, nq * d))
-    need = _tree_workspace(T, (past + 127) // 128, nq, nkv, d)
-    if workspace is None and stream is None:
-        size = max(need, 256)
-        ws = qkv.new_empty((size + 1) // 2)
-    else:
+    need = _tree_workspace(name, T, (past + 127) // 128, nq, nkv, d)
+    ws_ptr, size = None, 0
+    if workspace is not None or need > 0:
         ws = _workspace(workspace, need, qkv, dev, stream)
-        size = ws.numel() * ws.element_size()
+        ws_ptr, size = ws.data_ptr(), ws.numel() * ws.element_size()
     st = getattr(load(), name)(
         _ptr_typed(qkv, "qkv", dev, torch.bfloat16), *cache_ptrs, mask, T, past, max_len, nq, nkv,
-        d, int(tp_degree), _ptr_typed(ctx, "ctx", dev, torch.bfloat16), ws.data_ptr(), size,
+        d, int(tp_degree), _ptr_typed(ctx, "ctx", dev, torch.bfloat16), ws_ptr, size,
         _stream(stream))
     _check(st, name)
     return ctx

@@ -980,6 +980,14 @@ tp_status plan_tree(int T, int past, int nq, int nkv, bool k8, tpb::TreeParams& 
   return TP_OK;
 }
 
+// Bytes of a call's partials; 0 for arguments out of range.
+size_t tree_bytes(int T, int past, int nq, int nkv, int d, bool k8) {
+  if (!heads_ok(T, past, nq, nkv) || d != tpb::kAttnHeadDim) return 0;
+  tpb::TreeParams p;
+  size_t po = 0, pml = 0;
+  return plan_tree(T, past, nq, nkv, k8, p, po, pml) == TP_OK ? po + pml : 0;
+}
+
 template <bool k8>
 tp_status run_tree(const tp_bf16* qkv, void* k_cache, float* k_scale, void* v_cache, float* v_scale,
                    const uint64_t* mask, int T, int past, int max_len, int nq, int nkv, int d,
@@ -1654,15 +1662,14 @@ tp_status tp_tree_mask(const int32_t* parents, int T, uint64_t* mask) {
 }
 
 size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads, int head_dim) {
-  if (!heads_ok(T, past, n_q_heads, n_kv_heads) || head_dim != tpb::kAttnHeadDim) return 0;
-  size_t most = 0;
-  for (const bool k8 : {false, true}) {
-    tpb::TreeParams p;
-    size_t po = 0, pml = 0;
-    if (plan_tree(T, past, n_q_heads, n_kv_heads, k8, p, po, pml) != TP_OK) return 0;
-    most = po + pml > most ? po + pml : most;
-  }
-  return most;
+  const size_t bf16 = tree_bytes(T, past, n_q_heads, n_kv_heads, head_dim, false);
+  const size_t k8 = tree_bytes(T, past, n_q_heads, n_kv_heads, head_dim, true);
+  return bf16 > k8 ? bf16 : k8;
+}
+
+size_t tp_attn_decode_kv8_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads,
+                                          int head_dim) {
+  return tree_bytes(T, past, n_q_heads, n_kv_heads, head_dim, true);
 }
 
 tp_status tp_attn_tree(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,

@@ -153,6 +153,16 @@ def test_tree_workspace():
             assert f(T, past, 64, 8, 128) < 128 << 20
 
 
+def test_8_bit_workspace():
+    both, own = tp.tp_attn_tree_workspace_bytes, tp.tp_attn_decode_kv8_workspace_bytes
+    for T in (1, 4, 8, 9, 33, 128):
+        for past in (0, 1, 128, 1000, 2048, 2049, 65536):
+            for nq, nkv in ((8, 2), (64, 8), (28, 4), (16, 1), (64, 64)):
+                assert 0 <= own(T, past, nq, nkv, 128) <= both(T, past, nq, nkv, 128)
+    assert own(1, 1000, 64, 8, 128) == 0 and own(1, 65536, 64, 8, 128) > 0
+    assert own(129, 5, 8, 2, 128) == 0 and own(4, 5, 8, 2, 64) == 0
+
+
 def test_tree_mask_pointers(lib):
     p = (ctypes.c_int32 * 2)(-1, 0)
     m = (ctypes.c_uint64 * 2)()
