@@ -162,7 +162,7 @@ def _device(t: torch.Tensor) -> torch.device:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
     dev = t.device
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()  # there is a CUDA tensor: nothing to initialise
     if dev.index != cur:
         raise ValueError(f"inputs are on {dev} but the current device is cuda:{cur}; "
                          f"call under torch.cuda.device({dev.index})")
@@ -172,7 +172,7 @@ def _device(t: torch.Tensor) -> torch.device:
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is None:
         # the handle itself: a torch.cuda.Stream object costs 3 us to build
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if stream.device.index != torch.cuda.current_device():
         raise ValueError(f"stream is on {stream.device}, not the current device")
     return stream.cuda_stream
@@ -524,17 +524,26 @@ def _expect_shape(t: Optional[torch.Tensor], name: str, shape) -> None:
 def _qk_args(qkv, gamma_q, gamma_k, inv_freq, positions, n_q_heads, n_kv_heads, head_dim, dev):
     """Shape checks shared by tp_qk_norm_rope and its gradient; the pointers of
     the gains, the frequencies and the positions, and rot_dim."""
-    if qkv.dim() != 2 or qkv.shape[1] != (n_q_heads + 2 * n_kv_heads) * head_dim:
+    shape = qkv.shape
+    if len(shape) != 2 or shape[1] != (n_q_heads + 2 * n_kv_heads) * head_dim:
         raise ValueError("qkv must be [T, (nq + 2 nkv) d]")
-    _expect_shape(gamma_q, "gamma_q", (head_dim,))
-    _expect_shape(gamma_k, "gamma_k", (head_dim,))
-    _expect_shape(positions, "positions", (qkv.shape[0],))
-    if inv_freq is not None and inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot_dim / 2]")
-    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    return (_ptr(gamma_q, "gamma_q", dev), _ptr(gamma_k, "gamma_k", dev),
-            _ptr_typed(inv_freq, "inv_freq", dev, torch.float32) if rot else None,
-            _ptr_typed(positions, "positions", dev, torch.int32), rot)
+    gq = gk = fr = pos = None
+    rot = 0
+    if gamma_q is not None or gamma_k is not None:
+        _expect_shape(gamma_q, "gamma_q", (head_dim,))
+        _expect_shape(gamma_k, "gamma_k", (head_dim,))
+        gq = _ptr_typed(gamma_q, "gamma_q", dev, torch.bfloat16)
+        gk = _ptr_typed(gamma_k, "gamma_k", dev, torch.bfloat16)
+    if positions is not None:
+        _expect_shape(positions, "positions", (shape[0],))
+        pos = _ptr_typed(positions, "positions", dev, torch.int32)
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rot_dim / 2]")
+        rot = 2 * inv_freq.shape[0]
+        if rot:
+            fr = _ptr_typed(inv_freq, "inv_freq", dev, torch.float32)
+    return gq, gk, fr, pos, rot
 
 
 def _layout(layout) -> int:
