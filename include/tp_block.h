@@ -458,8 +458,9 @@ tp_status tp_attn_tree(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,
  * scales are split into three E5M2 terms (relative error 2^-9, or 2^-22 of the
  * largest weight times the largest value scale of a chunk of the cache); above
  * that the value codes are converted to fp16 and the weights times the scales are
- * fp16 (2^-11, or 2^-27 of the largest product of a chunk).  A query head that
- * holds an infinity gives NaN.  Other arguments, checks and errors as
+ * fp16 (2^-11, or 2^-27 of the largest product of a chunk).  Both hold for rows of
+ * values whose largest is from 2^-80 to 2^80, and rows of zeros; the terms of
+ * smaller ones end sooner.  A query head that holds an infinity gives NaN.  Other arguments, checks and errors as
  * tp_attn_tree.
  */
 tp_status tp_attn_decode_kv8(const tp_bf16* qkv, uint8_t* k_cache, float* k_scale, uint8_t* v_cache,

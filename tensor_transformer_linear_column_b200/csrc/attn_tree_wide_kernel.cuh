@@ -50,8 +50,10 @@ __host__ __device__ constexpr int wide_threads(bool k8) { return 32 * wide_first
 constexpr int kWideMaxStages = 10;
 constexpr float kWideSumMax = 1048576.0f;       // bf16: 64 keys' sum of weights up to 2^20
 constexpr float kWideProductMax = 60000.0f;     // 8 bits: products are fp16
-constexpr float kWideProductLog2 = 2.0f;        // a raise leaves products up to 2^2
-constexpr float kWideSumMaxKv8 = 1.2676506e30f; // 2^100
+constexpr float kWideProductLog2 = 2.0f;        // a raise leaves products up to 2^2 and
+constexpr float kWideWeightLog2 = 94.0f;        // weights up to 2^94: with that, products of
+constexpr float kWideSumMaxKv8 = 1.2676506e30f; // value scales from 2^-92 on stay there, and
+                                                // 64 weights' sum within 2^100
 
 template <bool k8, bool kShared>
 struct WideShape {
@@ -481,8 +483,7 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
                 }
               }
             }
-            // 8 bits: products up to 2^2, and no weight above 2^60
-            float mn = k8 ? fmaxf(product - kWideProductLog2, high - 60.0f) : high;
+            float mn = k8 ? fmaxf(product - kWideProductLog2, high - kWideWeightLog2) : high;
             mn = need ? fmaxf(m, mn) : m;
             // in two steps: an 8-bit row's m may rise by more than fp32's exponents
             const float part = exp2f(0.5f * (m - mn));
