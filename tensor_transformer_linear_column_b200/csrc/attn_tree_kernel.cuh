@@ -498,7 +498,8 @@ __device__ __forceinline__ void merge_tokens(MergeState& st, const TreeMergePara
         s[k] = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, q.w * kv.w)));
       }
       const float dot = warp_rows_reduce<kMergeTokens, false>(s, lane);
-      const float t = slot < count ? dot * ks * f : neg_inf();
+      // rounded once, for the maximum and for the exponents alike
+      const float t = slot < count ? __fmul_rn(dot * ks, f) : neg_inf();
       float high = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
       high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 16));
       const float ref = merge_raise(st, high);
@@ -827,7 +828,10 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
       tc_fence_after();
       const uint32_t s_at = tmem + lane_addr + static_cast<uint32_t>(slot * kSlotCols + c0);
       // e: scores in base-2 units over the running maximum, which stays unless
-      // some e passes kLazyLog2
+      // some e passes kLazyLog2.  The product is rounded before the maximum is taken
+      // off, as the maximum was: fused, the best key would keep that rounding, up to 8 in
+      // its weight's exponent where q . k is 2^30.  (The second rounding costs 0.15 us
+      // of 34.6 for 4 tokens over 65536 in 8 bits.)
       float2 e[kCols / 2];
       float over = kUnsetMax;
       auto scores = [&] {
@@ -862,7 +866,8 @@ __global__ void __launch_bounds__(TreeShape<kRows, k8>::kThreads, TreeShape<kRow
         scores();
 #pragma unroll
         for (int j = 0; j < kCols / 2; ++j)
-          e[j] = fma2(e[j], factor(j), *reinterpret_cast<const float2*>(nm_s + c0 + 2 * j));
+          e[j] = add2_unfused(mul2(e[j], factor(j)),
+                              *reinterpret_cast<const float2*>(nm_s + c0 + 2 * j));
         hide();
       };
       excess();
@@ -1298,8 +1303,9 @@ __global__ void __launch_bounds__(kManyWarps * 32)
     const bool see0 = j0 + lane < seen, see1 = j0 + lane + 32 < seen;
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
-      const float s0 = see0 ? (acc[0][k].x + acc[0][k].y) * by[0] : neg_inf();
-      const float s1 = see1 ? (acc[1][k].x + acc[1][k].y) * by[1] : neg_inf();
+      // rounded once, for the maximum and for the exponents alike
+      const float s0 = see0 ? __fmul_rn(acc[0][k].x + acc[0][k].y, by[0]) : neg_inf();
+      const float s1 = see1 ? __fmul_rn(acc[1][k].x + acc[1][k].y, by[1]) : neg_inf();
       float high = fmaxf(s0, s1);
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, x));

@@ -54,6 +54,12 @@ constexpr float kWideProductLog2 = 2.0f;        // a raise leaves products up to
 constexpr float kWideWeightLog2 = 94.0f;        // weights up to 2^94: with that, products of
 constexpr float kWideSumMaxKv8 = 1.2676506e30f; // value scales from 2^-92 on stay there, and
                                                 // 64 weights' sum within 2^100
+// Above this a row's scores (in base-2 units) are far: a score is rounded before m is
+// taken off, as m was.  In one fused step the best key would keep that rounding, up to
+// 8 in its weight's exponent from 2^27 on.  And over 8 bits the range of the products
+// is an offset c beside m, which m + c would lose.  Two operations instead of one for
+// every score cost 0.4 us of 22.3 (26 tokens of 64 / 8 heads over 8191).
+constexpr float kWideFarScore = 1048576.0f;     // 2^20: m is held to 2^-4
 
 template <bool k8, bool kShared>
 struct WideShape {
@@ -365,7 +371,9 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
     const int mine = kShared ? nbc : (nbc - t + 1) / 2;  // this tile's units
     auto key_of = [&](int k) { return key0 + (kShared ? k : 2 * k + t) * 128; };
 
-    float m = kUnsetMax, l = 0.0f;
+    float m = kUnsetMax, l = 0.0f;  // weights are 2^(score - m - c); c is 0 but for 8 bits
+    float c = 0.0f;                 // and far scores
+    bool far = false;               // any of the warp's rows
     bool ok = true;
     float k_next = 0.0f, v_next = 0.0f;
     const size_t sc_row = static_cast<size_t>(g) * p.max_len + r;
@@ -395,32 +403,32 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
       }
       ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&s_full[t]), k & 1, abort_flag));
       tc_fence_after();
-      // 32 raw scores from column c on
-      auto fetch = [&](int c, uint32_t (&sv)[32]) {
+      // 32 raw scores from column `col` on
+      auto fetch = [&](int col, uint32_t (&sv)[32]) {
         if (ok) {
-          tmem_ld32(s_at + static_cast<uint32_t>(c), sv);
+          tmem_ld32(s_at + static_cast<uint32_t>(col), sv);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) sv[j] = 0u;
         }
       };
-      // ... in base-2 units less `base`; behind the cache's last key: -inf
-      auto scaled = [&](const uint32_t (&sv)[32], int c, float base, bool tail, float2 (&e)[16]) {
-        const float2 f = make_float2(rf, rf), nb = make_float2(-base, -base);
+      // ... in base-2 units
+      auto factor = [&](int col) {
+        const float2 f = make_float2(rf, rf);
+        return k8 ? mul2(f, *reinterpret_cast<const float2*>(ks + col)) : f;
+      };
+      auto products = [&](const uint32_t (&sv)[32], int col, float2 (&e)[16]) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          e[j] = mul2(make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])),
+                      factor(col + 2 * j));
+      };
+      // behind the cache's last key: -inf
+      auto hide = [&](int col, float2 (&e)[16]) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float2 s = make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
-          if constexpr (k8)
-            e[j] = fma2(s, mul2(f, *reinterpret_cast<const float2*>(ks + c + 2 * j)), nb);
-          else
-            e[j] = fma2(s, f, nb);
-        }
-        if (tail) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c + 2 * j >= left) e[j].x = neg_inf();
-            if (c + 2 * j + 1 >= left) e[j].y = neg_inf();
-          }
+          if (col + 2 * j >= left) e[j].x = neg_inf();
+          if (col + 2 * j + 1 >= left) e[j].y = neg_inf();
         }
       };
       // The block's halves of 64 keys in turn: weights with the running m, their sum
@@ -434,61 +442,104 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
         float2 acc;
         float top;
         uint32_t pk[32];
-        auto weights32 = [&](const uint32_t (&sv)[32], int c, bool tail) {  // keys base + c ...
+        auto weights32 = [&](const uint32_t (&sv)[32], int col, auto careful) {  // keys base + col ...
           float2 e[16];
-          scaled(sv, base + c, m, tail, e);
+          const float2 nm = make_float2(-m, -m);
+          if constexpr (careful) {  // far scores, or the cache's end
+            products(sv, base + col, e);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              e[j] = add2_unfused(e[j], nm);
+              if constexpr (k8) e[j] = add2(e[j], make_float2(-c, -c));
+            }
+            hide(base + col, e);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              e[j] = fma2(make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])),
+                          factor(base + col + 2 * j), nm);
+          }
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             e[j] = make_float2(exp2_fast(e[j].x), exp2_fast(e[j].y));
             acc = add2(acc, e[j]);
             if constexpr (k8) {
-              e[j] = mul2(e[j], *reinterpret_cast<const float2*>(ks + 128 + base + c + 2 * j));
+              e[j] = mul2(e[j], *reinterpret_cast<const float2*>(ks + 128 + base + col + 2 * j));
               top = fmaxf(top, fmaxf(e[j].x, e[j].y));
               const __half2 h = __float22half2_rn(e[j]);
-              pk[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
+              pk[col / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
             } else {
-              pk[c / 2 + j] = pack_bf16x2(e[j].x, e[j].y);
+              pk[col / 2 + j] = pack_bf16x2(e[j].x, e[j].y);
             }
           }
         };
-        auto weights = [&](auto tail) {
+        auto weights = [&](auto careful) {
           uint32_t sa[32], sb[32];
           acc = make_float2(0.0f, 0.0f);
           top = 0.0f;
           fetch(base, sa);
           tmem_wait_ld();
           fetch(base + 32, sb);  // on their way meanwhile
-          weights32(sa, 0, tail);
+          weights32(sa, 0, careful);
           tmem_wait_ld();
-          weights32(sb, 32, tail);
+          weights32(sb, 32, careful);
         };
         bool need = k + half == 0, raised = false;
         for (;;) {
           if (__any_sync(0xffffffffu, need)) {
             raised = true;
-            float high = kUnsetMax, product = kUnsetMax;
+            // the scores' maximum, and (8 bits) that of the products; where scores are
+            // far once more, over that maximum
+            float high = kUnsetMax, product = kUnsetMax, anchor = 0.0f;
+            bool is_far = false;
 #pragma unroll 1
-            for (int c = base; c < base + 64; c += 32) {
-              uint32_t sv[32];
-              float2 e[16];
-              fetch(c, sv);
-              tmem_wait_ld();
-              scaled(sv, c, 0.0f, left < 128, e);
+            for (int pass = 0; pass < 2; ++pass) {
+              float top_score = kUnsetMax;
+              product = kUnsetMax;
+#pragma unroll 1
+              for (int col = base; col < base + 64; col += 32) {
+                uint32_t sv[32];
+                float2 e[16];
+                fetch(col, sv);
+                tmem_wait_ld();
+                products(sv, col, e);
+                if (k8 && pass > 0) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                high = fmaxf(high, fmaxf(e[j].x, e[j].y));
-                if constexpr (k8) {
-                  const float2 lv = *reinterpret_cast<const float2*>(ks + 256 + c + 2 * j);
-                  product = fmaxf(product, fmaxf(e[j].x + lv.x, e[j].y + lv.y));
+                  for (int j = 0; j < 16; ++j) e[j] = add2_unfused(e[j], make_float2(-anchor, -anchor));
+                }
+                if (left < 128) hide(col, e);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  top_score = fmaxf(top_score, fmaxf(e[j].x, e[j].y));
+                  if constexpr (k8) {
+                    const float2 lv = *reinterpret_cast<const float2*>(ks + 256 + col + 2 * j);
+                    product = fmaxf(product, fmaxf(e[j].x + lv.x, e[j].y + lv.y));
+                  }
                 }
               }
+              if (pass > 0) break;
+              high = top_score;
+              is_far = fabsf(high) > kWideFarScore && high != kUnsetMax;
+              if (!k8 || !__any_sync(0xffffffffu, is_far)) break;
+              anchor = is_far ? high : 0.0f;
             }
-            float mn = k8 ? fmaxf(product - kWideProductLog2, high - kWideWeightLog2) : high;
-            mn = need ? fmaxf(m, mn) : m;
-            // in two steps: an 8-bit row's m may rise by more than fp32's exponents
-            const float part = exp2f(0.5f * (m - mn));
+            float mn = high, cn = 0.0f;
+            if constexpr (k8) {
+              const float by = fmaxf(product - kWideProductLog2,
+                                     (is_far ? 0.0f : high) - kWideWeightLog2);
+              if (is_far)
+                cn = rintf(by);  // a power of two, for the partial
+              else
+                mn = by;
+            }
+            const float rise = (mn - m) + (cn - c);
+            const bool up = need && rise > 0.0f;
+            // in two steps: an 8-bit row's reference may rise by more than fp32's exponents
+            const float part = up ? exp2f(-0.5f * rise) : 1.0f;
             l = l * part * part;
-            m = mn;
+            m = up ? mn : m;
+            c = up ? cn : c;
+            far = __any_sync(0xffffffffu, fabsf(m) > kWideFarScore && m != kUnsetMax);
             // O holds the products of the tile's earlier units and of this one's
             // first half: wait for that one
             if (half == 1)
@@ -496,19 +547,19 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
             if (k + half > 0 && ok) {
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < 128; c += 16) {
+              for (int col = 0; col < 128; col += 16) {
                 uint32_t o[16];
-                tmem_ld16(o_at + static_cast<uint32_t>(c), o);
+                tmem_ld16(o_at + static_cast<uint32_t>(col), o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                   o[j] = __float_as_uint(__uint_as_float(o[j]) * part * part);
-                tmem_st16(o_at + static_cast<uint32_t>(c), o);
+                tmem_st16(o_at + static_cast<uint32_t>(col), o);
               }
               tmem_wait_st();
             }
           }
-          if (left < 128)
+          if (left < 128 || far)
             weights(std::true_type{});
           else
             weights(std::false_type{});
@@ -534,9 +585,12 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
       ok = __all_sync(0xffffffffu, ok && wait_parity(smem_u32(&o_done[x]), 0, abort_flag));
     tc_fence_after();
     // the partial, with the sum brought to [1, 2): m then stands for the row's
-    // mass whatever the value scales were
+    // mass whatever the value scales were.  A far row's m cannot take that in: its sum
+    // is left (its best weight was 1 at the last raise), but for c
+    const bool far_row = fabsf(m) > kWideFarScore;
     const int le = static_cast<int>((__float_as_uint(l) >> 23) & 0xFFu) - 127;
-    const int shift = l > 0.0f && le > -127 && le < 128 ? (le < -126 ? -126 : le > 126 ? 126 : le) : 0;
+    int shift = l > 0.0f && le > -127 && le < 128 ? (le < -126 ? -126 : le > 126 ? 126 : le) : 0;
+    if (far_row) shift = -static_cast<int>(c);
     const float down = pow2i(-shift);
     const size_t part = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks * (kShared ? 1 : 2) +
                         (kShared ? chunk : 2 * chunk + t);
@@ -544,7 +598,7 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
     const bool in = row0 + r < p.R;
     if (in)
       *reinterpret_cast<float2*>(p.part_ml + out_row * 2) =
-          make_float2(m + static_cast<float>(shift), l * down);
+          make_float2(far_row ? m : m + static_cast<float>(shift), l * down);
     // O row by row: a warp turns 64 columns of its 32 rows at a time through 8 KB
     // of the ring, which is empty by now (16-byte piece c of row r at c ^ (r % 16)),
     // so that 16 lanes write 256 contiguous bytes

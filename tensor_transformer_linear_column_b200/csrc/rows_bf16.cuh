@@ -35,6 +35,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&r);
 }
 
+// add2 where a product in front keeps its rounding: the assembler fuses a packed
+// product and sum, .rn or not, but not these.
+__device__ __forceinline__ float2 add2_unfused(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
 // This warp's index in the block, known to be the same in all its lanes: where loops
 // and branches depend on threadIdx directly, the compiler reconverges the warp
 // around every shuffle in them (300 cycles each).
