@@ -1227,8 +1227,8 @@ __global__ void __launch_bounds__(kManyWarps * 32)
 #pragma unroll
   for (int k = 0; k < kHeads; ++k) {
     const int h = h0 + k < p.G ? h0 + k : p.G - 1;
-    reinterpret_cast<float4*>(wq)[k * 32 + lane] = cache_values<false>(__ldg(
-        reinterpret_cast<const uint2*>(p.qkv + i * ld + (g * p.G + h) * kAttnHeadDim) + lane));
+    reinterpret_cast<float4*>(wq)[k * 32 + lane] = cache_values<false>(
+        reinterpret_cast<const uint2*>(p.qkv + i * ld + (g * p.G + h) * kAttnHeadDim)[lane]);
   }
   load_chunks(0);  // on their way under the new tokens' work
   asm volatile("cp.async.wait_all;" ::: "memory");

@@ -416,12 +416,13 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_norm_rope_kernel(const QkPar
     }
     __syncwarp();
   } else if (p.rot > 0) {
-    // ---------------- angles, up to kQkStages tokens ahead
+    // ---------------- angles, up to kQkStages tokens ahead.  Plain loads: the kernel
+    // before this one may have written the frequencies and the positions
     const int half = p.rot / 2;
     float freq[kQkMaxDim / 64];
 #pragma unroll
     for (int j = 0; j < kQkMaxDim / 64; ++j)
-      freq[j] = lane + 32 * j < half ? __ldg(p.inv_freq + lane + 32 * j) : 0.0f;
+      freq[j] = lane + 32 * j < half ? p.inv_freq[lane + 32 * j] : 0.0f;
     for (int k = 0; k < tokens; ++k) {
       const int st = k % kQkStages;
       const int token = static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x);
