@@ -407,11 +407,19 @@ tp_status tp_tree_mask(const int32_t* parents, int T, uint64_t* mask);
  * tokens after `past` cached ones; 0 for past = 0 and for unsupported
  * arguments.  A function of the sizes only.  The second is what
  * tp_attn_decode_kv8 alone needs: never more, and 0 also for a short cache whose
- * partial results stay on chip.
+ * partial results stay on chip.  Either may fall as `past` grows (a cache is cut
+ * into chunks that fill the GPU, and a longer one may make fewer): what a final
+ * length needs does not cover every length on the way.  One buffer for a growing
+ * cache takes the third, enough for both calls after any number of cached tokens
+ * up to max_past.
  */
 size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads, int head_dim);
 size_t tp_attn_decode_kv8_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads,
                                           int head_dim);
+size_t tp_attn_tree_workspace_bytes_upto(int T, int max_past, int n_q_heads, int n_kv_heads,
+                                         int head_dim);
+size_t tp_attn_tree_workspace_bytes_upto(int T, int max_past, int n_q_heads, int n_kv_heads,
+                                         int head_dim);
 
 /*
  * Attention of a tree of drafted tokens over a cache: tp_attn_decode with a

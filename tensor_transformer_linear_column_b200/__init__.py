@@ -66,6 +66,7 @@ SIGNATURES = {
     "tp_tree_mask": (_I, [_P, _I, _P]),
     "tp_attn_tree_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
     "tp_attn_decode_kv8_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
+    "tp_attn_tree_workspace_bytes_upto": (_Z, [_I, _I, _I, _I, _I]),
     "tp_attn_tree": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z, _P]),
     "tp_attn_decode_kv8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _Z,
                                 _P]),
@@ -731,6 +732,14 @@ def tp_attn_decode_kv8_workspace_bytes(T: int, past: int, n_q_heads: int, n_kv_h
                                        head_dim: int) -> int:
     return int(load().tp_attn_decode_kv8_workspace_bytes(int(T), int(past), int(n_q_heads),
                                                          int(n_kv_heads), int(head_dim)))
+
+
+def tp_attn_tree_workspace_bytes_upto(T: int, max_past: int, n_q_heads: int, n_kv_heads: int,
+                                      head_dim: int) -> int:
+    """Enough for tp_attn_tree and tp_attn_decode_kv8 after any number of cached
+    tokens up to max_past; what the two above give may fall as `past` grows."""
+    return int(load().tp_attn_tree_workspace_bytes_upto(int(T), int(max_past), int(n_q_heads),
+                                                        int(n_kv_heads), int(head_dim)))
 
 
 @functools.lru_cache(maxsize=256)

@@ -925,6 +925,16 @@ tp_status launch_append(const tpb::KvAppendParams& p, cudaStream_t stream) {
 // ------------------------------------------------------------------ attention of a few new tokens
 
 
+constexpr int kTreeChunks = 296, kTreeWaves = 4;  // chunks and waves of blocks that a plan takes
+
+// Bytes of the partials of p.chunks chunks.
+void tree_partials(const tpb::TreeParams& p, const TreeLaunch& l, size_t& part_o_bytes,
+                   size_t& part_ml_bytes) {
+  const size_t rows = static_cast<size_t>(p.groups) * p.nkv * p.chunks * l.partials * l.rows;
+  part_o_bytes = rows * tpb::kAttnHeadDim * 4;
+  part_ml_bytes = (rows * 2 * 4 + 255) / 256 * 256;
+}
+
 // Chunks per head: the fewest key blocks on the busiest SM, counting three for a
 // block's set-up and partial.
 tp_status plan_tree(int T, int past, int nq, int nkv, bool k8, tpb::TreeParams& p,
@@ -960,12 +970,12 @@ tp_status plan_tree(int T, int past, int nq, int nkv, bool k8, tpb::TreeParams& 
     const long long slots = static_cast<long long>(kTreeSms) * l.blocks_per_sm;
     const long long per_chunk = static_cast<long long>(nkv) * p.groups;
     long long best = 0;
-    const int most = p.nblk < 296 ? p.nblk : 296;
+    const int most = p.nblk < kTreeChunks ? p.nblk : kTreeChunks;
     for (int c = 1; c <= most; ++c) {
       const int nb = (p.nblk + c - 1) / c;
       const int chunks = (p.nblk + nb - 1) / nb;
       const long long waves = (per_chunk * chunks + slots - 1) / slots;
-      if (waves > 4 && best != 0) break;  // more chunks only add partials
+      if (waves > kTreeWaves && best != 0) break;  // more chunks only add partials
       const long long cost = waves * (nb + 3);
       if (best == 0 || cost < best) {
         best = cost;
@@ -974,9 +984,7 @@ tp_status plan_tree(int T, int past, int nq, int nkv, bool k8, tpb::TreeParams& 
       }
     }
   }
-  const size_t rows = static_cast<size_t>(p.groups) * nkv * p.chunks * l.partials * l.rows;
-  part_o_bytes = rows * tpb::kAttnHeadDim * 4;
-  part_ml_bytes = (rows * 2 * 4 + 255) / 256 * 256;
+  tree_partials(p, l, part_o_bytes, part_ml_bytes);
   return TP_OK;
 }
 
@@ -986,6 +994,22 @@ size_t tree_bytes(int T, int past, int nq, int nkv, int d, bool k8) {
   tpb::TreeParams p;
   size_t po = 0, pml = 0;
   return plan_tree(T, past, nq, nkv, k8, p, po, pml) == TP_OK ? po + pml : 0;
+}
+
+// Enough for every `past` up to max_past: a plan has as many chunks as blocks of keys
+// at most, as kTreeChunks, and (but for one chunk) as fit kTreeWaves waves.
+size_t tree_bytes_upto(int T, int max_past, int nq, int nkv, int d, bool k8) {
+  if (!heads_ok(T, max_past, nq, nkv) || d != tpb::kAttnHeadDim) return 0;
+  tpb::TreeParams p;
+  size_t po = 0, pml = 0;
+  if (plan_tree(T, max_past, nq, nkv, k8, p, po, pml) != TP_OK || p.nblk == 0) return 0;
+  const TreeLaunch& l = tree_launch_for(p.R, k8);
+  const long long fit = static_cast<long long>(kTreeWaves) * kTreeSms * l.blocks_per_sm /
+                        (static_cast<long long>(nkv) * p.groups);
+  p.chunks = p.nblk < kTreeChunks ? p.nblk : kTreeChunks;
+  if (p.chunks > fit) p.chunks = fit < 1 ? 1 : static_cast<int>(fit);
+  tree_partials(p, l, po, pml);
+  return po + pml;
 }
 
 template <bool k8>
@@ -1670,6 +1694,13 @@ size_t tp_attn_tree_workspace_bytes(int T, int past, int n_q_heads, int n_kv_hea
 size_t tp_attn_decode_kv8_workspace_bytes(int T, int past, int n_q_heads, int n_kv_heads,
                                           int head_dim) {
   return tree_bytes(T, past, n_q_heads, n_kv_heads, head_dim, true);
+}
+
+size_t tp_attn_tree_workspace_bytes_upto(int T, int max_past, int n_q_heads, int n_kv_heads,
+                                         int head_dim) {
+  const size_t bf16 = tree_bytes_upto(T, max_past, n_q_heads, n_kv_heads, head_dim, false);
+  const size_t k8 = tree_bytes_upto(T, max_past, n_q_heads, n_kv_heads, head_dim, true);
+  return bf16 > k8 ? bf16 : k8;
 }
 
 tp_status tp_attn_tree(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,
