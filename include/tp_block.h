@@ -463,13 +463,13 @@ tp_status tp_attn_tree(const tp_bf16* qkv, tp_bf16* k_cache, tp_bf16* v_cache,
  * queries are split into two E4M3 terms (exact for elements of at least 2^-9
  * of their head's largest, within 2^-17 of the largest below that).  Up to 64
  * query rows per key-value head (T nq / nkv), softmax weights times the values'
- * scales are split into three E5M2 terms (relative error 2^-9, or 2^-22 of the
- * largest weight times the largest value scale of a chunk of the cache); above
- * that the value codes are converted to fp16 and the weights times the scales are
- * fp16 (2^-11, or 2^-27 of the largest product of a chunk).  Both hold for rows of
- * values whose largest is from 2^-80 to 2^80, and rows of zeros; the terms of
- * smaller ones end sooner.  A query head that holds an infinity gives NaN.  Other arguments, checks and errors as
- * tp_attn_tree.
+ * scales are split into three E5M2 terms (each within 2^-9 + 2^-11 of itself plus
+ * 2^-21 of the largest weight times the largest value scale of a chunk of the
+ * cache); above that the value codes are converted to fp16 and the weights times
+ * the scales are fp16 (within 2^-11, plus 2^-26 of the largest product of a chunk).
+ * Both hold for rows of values whose largest is from 2^-80 to 2^80, and rows of
+ * zeros; smaller ones keep fewer bits.  A query head that holds an infinity gives
+ * NaN.  Other arguments, checks and errors as tp_attn_tree.
  */
 tp_status tp_attn_decode_kv8(const tp_bf16* qkv, uint8_t* k_cache, float* k_scale, uint8_t* v_cache,
                              float* v_scale, const uint64_t* tree_mask, int T, int past,

@@ -48,10 +48,10 @@
 //     2^-9 of the row's largest and within 2^-17 of the largest below that
 //   - a weight p is multiplied by its key's value scale over C, a power of two
 //     at or above every value scale of the chunk so far (a running maximum, raised
-//     like m), and by 2^5, and becomes the sum of three E5M2 terms of 3 bits each:
-//     relative error 2^-9, as a bf16 weight has, or 2^-22 of the largest weight
-//     times C where that is more.  E5M2 is the upper byte of fp16, so the split is
-//     masks and exact subtractions in fp16 pairs
+//     like m), and by 2^5, rounded to fp16, and becomes the sum of three E5M2 terms of
+//     3 bits each: within 2^-9 + 2^-11 of itself (a bf16 weight: 2^-9), plus 2^-22 of
+//     the largest weight times C, where the terms end.  E5M2 is the upper byte of
+//     fp16, so the split is masks and exact subtractions in fp16 pairs
 // Keys' scales multiply the scores, one per lane.  Sums of weights are of the
 // unrounded ones, in fp32.
 //
@@ -366,7 +366,7 @@ __device__ __forceinline__ void append_pass(const TreeParams& p, int g, int part
   }
 }
 
-// 16 weights (already times 2^11 times the value scale over C) as three 16-byte
+// 16 weights (already times 2^5 times the value scale over C) as three 16-byte
 // vectors of E5M2 terms: a = the leading 3 bits, b = the next of the rest, c =
 // the rest of that, rounded.  x - a and x - a - b are exact in fp16.
 __device__ __forceinline__ void split_weights(const float2* w, uint4& a4, uint4& b4, uint4& c4) {

@@ -32,10 +32,11 @@
 // 8-bit caches: scores as in attn_tree_kernel (queries in two E4M3 parts against
 // the codes); here two more warps turn each block's value codes into fp16 once for
 // all rows, and a row's weights times the value scales are fp16 against those
-// (relative error 2^-11, or 2^-27 of the largest product; splitting them into three
-// E5M2 terms, as for few rows, costs three of eight instructions an element: 266 us
-// instead of 184 for 64 tokens over 65536 rows).  A row's m bounds the products p * scale themselves, so a
-// key of a large value scale and a small weight costs the others nothing.
+// (within 2^-11, plus 2^-26 of the largest product; splitting them into three E5M2
+// terms, as for few rows, costs three of eight instructions an element: 266 us instead
+// of 184 for 64 tokens over 65536 rows).  A row's m bounds the products p * scale
+// themselves, so a key of a large value scale and a small weight costs the others
+// nothing.
 #pragma once
 
 #include <type_traits>

@@ -175,3 +175,37 @@ def test_values_that_are_all_small_or_all_large(eight, T, size):
     c.qkv = x.to(torch.bfloat16).reshape(T, -1)
     c.set_cache(k.to(torch.bfloat16), v.to(torch.bfloat16))
     c.check((T, size))
+
+
+@pytest.mark.parametrize("first", [7.0, 7.37, 7.71])
+@pytest.mark.parametrize("high", [450.0, 894.0])
+def test_many_small_weights_under_one_large_in_8_bits(high, first):
+    # Up to 64 rows over 8 bits: a weight times its value scale is held to 2^-9 + 2^-11
+    # of itself (three terms of three bits, of an fp16 number) plus 2^-22 of C for a
+    # largest weight of 1 (where the terms end), C the power of two at or above the
+    # chunk's largest scale -- here just below and twice that scale.  127 keys of one
+    # weight: their errors have one sign and add up.
+    nq, past = 16, 128
+    c = Case(True, 1, past, nq, 1, "any", seed=1)
+    c.words = torch.zeros(1, 1, dtype=torch.int64)  # the cached keys alone
+    q = torch.zeros(nq + 2, D)
+    log2 = first + 0.83 * torch.arange(nq)          # the weights: 2^-7 .. 2^-20
+    q[:nq, 0] = log2 * np.sqrt(D) / np.log2(np.e)
+    c.qkv = q.to(torch.bfloat16).reshape(1, -1)
+    k = torch.zeros(1, past + 4, D)
+    k[:, :past - 1, 0] = -1.0
+    v = torch.full((1, past + 4, D), high)
+    v[:, past - 1, 1:] = 0                           # the large one is seen in element 0 alone
+    c.set_cache(k.to(torch.bfloat16), v.to(torch.bfloat16))
+    _, scale = c.cache[2:]
+    top = float(scale[:, :past].max())
+    power = 2.0 ** np.ceil(np.log2(top))
+    ref, _ = c.reference()
+    y = c.run()[0].double().cpu().numpy().reshape(nq, D)[:, 1:]
+    ref = ref.reshape(nq, D)[:, 1:]
+    total = ref[:, :1] / high                        # the small weights over the sum of all
+    small = total / (past - 1) / (1 - total)         # one of them, the large one being 1
+    each = ((2.0 ** -9 + 2.0 ** -11) * small * top + 2.0 ** -22 * power) * 448
+    # and 2^-17 of the weights for their scores and exponentials, 2^-8 for the result
+    bound = 2.0 ** -8 * ref + (1 - total) * (past - 1) * each + 2.0 ** -17 * ref
+    assert (np.abs(y - ref) <= bound * (1 + 2.0 ** -7)).all(), np.max(np.abs(y - ref) / bound)
