@@ -1,5 +1,5 @@
-// rows_bf16.cuh -- eight bf16 elements (16 bytes) of a row to fp32 and back, and
-// fp32 arithmetic on two values at a time.
+// rows_bf16.cuh -- eight bf16 elements (16 bytes) of a row to fp32, and fp32
+// arithmetic on two values at a time.
 #pragma once
 
 #include "ptx.cuh"
@@ -55,11 +55,6 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     f[2 * q] = __uint_as_float(w[q] << 16);
     f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
   }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
 }
 
 }  // namespace tpb
