@@ -772,8 +772,9 @@ bool make_tmap_rows3_u8(CUtensorMap* map, const void* base, uint64_t rows, uint6
 
 // ------------------------------------------------------------------ heads' rows (norms, caches)
 
+// (the kernels count a token's heads, nq + 2 nkv, in 32 bits)
 bool heads_ok(int T, int past, int nq, int nkv) {
-  return T >= 1 && past >= 0 && nq >= 1 && nkv >= 1 && nq % nkv == 0;
+  return T >= 1 && past >= 0 && nq >= 1 && nkv >= 1 && nq % nkv == 0 && nq <= INT_MAX - 2ll * nkv;
 }
 
 bool row_dim_ok(int d) { return d >= 16 && d <= tpb::kQkMaxDim && d % 16 == 0; }
