@@ -517,6 +517,14 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor,
     return workspace
 
 
+def _int32(value, name: str) -> int:
+    """A length or position as the C int it is passed as (ctypes would wrap it)."""
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
+
+
 def _expect_shape(t: Optional[torch.Tensor], name: str, shape) -> None:
     if t is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -563,6 +571,7 @@ def tp_qk_norm_rope(qkv: torch.Tensor, past: int, n_q_heads: int, n_kv_heads: in
     qkv [T, (nq + 2 nkv) d] to a buffer of the same shape, which may be qkv
     itself (out=qkv).  Token i is at positions[i] (int32), or at past + i;
     layout "half" pairs (p, p + rot / 2), "pairs" (2 p, 2 p + 1)."""
+    past = _int32(past, "past")
     dev = _device(qkv)
     gq, gk, fr, pos, rot = _qk_args(qkv, gamma_q, gamma_k, inv_freq, positions, n_q_heads,
                                     n_kv_heads, head_dim, dev)
@@ -570,7 +579,7 @@ def tp_qk_norm_rope(qkv: torch.Tensor, past: int, n_q_heads: int, n_kv_heads: in
         out = torch.empty_like(qkv) if stream is None else _empty_on(qkv, qkv.shape, stream)
     else:
         _expect_shape(out, "out", qkv.shape)
-    st = load().tp_qk_norm_rope(_ptr(qkv, "qkv", dev), gq, gk, fr, pos, qkv.shape[0], int(past),
+    st = load().tp_qk_norm_rope(_ptr(qkv, "qkv", dev), gq, gk, fr, pos, qkv.shape[0], past,
                                 int(n_q_heads), int(n_kv_heads), int(head_dim), rot,
                                 _layout(layout), float(eps), int(tp_degree),
                                 _ptr(out, "out", dev), _stream(stream))
@@ -595,6 +604,7 @@ def tp_qk_norm_rope_backward(qkv: torch.Tensor, dout: torch.Tensor, past: int, n
     {"dqkv", "dgamma_q", "dgamma_k"} (the gains' None without norms).  qkv is the
     forward call's input, so a forward call that is to be differentiated must not
     run in place; dqkv may be dout itself."""
+    past = _int32(past, "past")
     dev = _device(qkv)
     gq, gk, fr, pos, rot = _qk_args(qkv, gamma_q, gamma_k, inv_freq, positions, n_q_heads,
                                     n_kv_heads, head_dim, dev)
@@ -611,7 +621,7 @@ def tp_qk_norm_rope_backward(qkv: torch.Tensor, dout: torch.Tensor, past: int, n
         ws = _workspace(workspace, tp_qk_norm_rope_backward_workspace_bytes(T, head_dim), qkv, dev,
                         stream)
     st = load().tp_qk_norm_rope_backward(
-        _ptr(qkv, "qkv", dev), gq, gk, fr, pos, _ptr(dout, "dout", dev), T, int(past),
+        _ptr(qkv, "qkv", dev), gq, gk, fr, pos, _ptr(dout, "dout", dev), T, past,
         int(n_q_heads), int(n_kv_heads), int(head_dim), rot, _layout(layout), float(eps),
         int(tp_degree), _ptr(dqkv, "dqkv", dev), _ptr(dgq, "dgamma_q", dev),
         _ptr(dgk, "dgamma_k", dev), None if ws is None else ws.data_ptr(),
@@ -628,7 +638,7 @@ def _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim):
     if len(shape) != 3 or shape != v_cache.shape or shape[0] != n_kv_heads or \
             shape[2] != head_dim:
         raise ValueError("caches must be [nkv, max_len, d]")
-    return rows[0], shape[1]
+    return rows[0], _int32(shape[1], "max_len")
 
 
 def _kv8_ptrs(k_cache, k_scale, v_cache, v_scale, shape, dev):
@@ -657,10 +667,11 @@ def tp_kv_append(qkv: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     """Write the keys and values of qkv's rows (int32 `rows` in that order, or all
     T) into the bf16 caches [nkv, max_len, d] from row `past` on, in place."""
     T, max_len = _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    past = _int32(past, "past")
     dev = _device(qkv)
     rp, n = _rows(rows, T, dev)
     _check(load().tp_kv_append(_ptr(qkv, "qkv", dev), rp, _ptr(k_cache, "k_cache", dev),
-                               _ptr(v_cache, "v_cache", dev), T, n, int(past),
+                               _ptr(v_cache, "v_cache", dev), T, n, past,
                                max_len, int(n_q_heads), int(n_kv_heads), int(head_dim),
                                int(tp_degree), _stream(stream)), "tp_kv_append")
 
@@ -673,12 +684,13 @@ def tp_kv8_append(qkv: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tenso
     """tp_kv_append into an 8-bit cache: E4M3 codes (uint8) [nkv, max_len, d] and
     fp32 scales [nkv, max_len], a row being scale * e4m3(code)."""
     T, max_len = _check_qkv_cache(qkv, k_cache, v_cache, n_q_heads, n_kv_heads, head_dim)
+    past = _int32(past, "past")
     dev = _device(qkv)
     rp, n = _rows(rows, T, dev)
     _check(load().tp_kv8_append(_ptr(qkv, "qkv", dev), rp,
                                 *_kv8_ptrs(k_cache, k_scale, v_cache, v_scale,
                                            (n_kv_heads, max_len), dev), T,
-                                n, int(past), max_len, int(n_q_heads), int(n_kv_heads),
+                                n, past, max_len, int(n_q_heads), int(n_kv_heads),
                                 int(head_dim), int(tp_degree), _stream(stream)), "tp_kv8_append")
 
 
@@ -691,10 +703,14 @@ def tp_kv8_read(k_cache: torch.Tensor, k_scale: torch.Tensor, v_cache: torch.Ten
     out_len = start + count, their rows before `start` unset."""
     if k_cache.dim() != 3 or tuple(k_cache.shape) != tuple(v_cache.shape):
         raise ValueError("caches must be [nkv, max_len, d]")
-    dev = _device(k_cache)
+    start, count = _int32(start, "start"), _int32(count, "count")
     nkv, max_len, d = k_cache.shape
+    _int32(max_len, "max_len")
+    dev = _device(k_cache)
+    # (a range past max_len is refused below: no memory for it)
     shape = tuple((k_out if k_out is not None else v_out).shape) \
-        if k_out is not None or v_out is not None else (nkv, max(int(start) + int(count), 1), d)
+        if k_out is not None or v_out is not None \
+        else (nkv, min(max(start + count, 1), max_len), d)
     if len(shape) != 3 or (shape[0], shape[2]) != (nkv, d):
         raise ValueError("k_out and v_out must be [nkv, out_len, d]")
     if k_out is None:
@@ -703,10 +719,9 @@ def tp_kv8_read(k_cache: torch.Tensor, k_scale: torch.Tensor, v_cache: torch.Ten
         v_out = _empty_on(k_cache, shape, stream, torch.bfloat16)
     _expect_shape(v_out, "v_out", k_out.shape)
     _check(load().tp_kv8_read(*_kv8_ptrs(k_cache, k_scale, v_cache, v_scale, (nkv, max_len), dev),
-                              int(start),
-                              int(count), max_len, nkv, d, int(tp_degree),
-                              _ptr(k_out, "k_out", dev), _ptr(v_out, "v_out", dev), shape[1],
-                              _stream(stream)), "tp_kv8_read")
+                              start, count, max_len, nkv, d, int(tp_degree),
+                              _ptr(k_out, "k_out", dev), _ptr(v_out, "v_out", dev),
+                              _int32(shape[1], "out_len"), _stream(stream)), "tp_kv8_read")
     return k_out, v_out
 
 
@@ -714,7 +729,7 @@ def tp_tree_mask(parents) -> torch.Tensor:
     """Visibility words of a drafted tree, int64 [T, ceil(T / 64)] on the host:
     token i sees itself and its ancestors; parents[i] < i is the parent of token
     i, or -1 (host arithmetic, no GPU needed)."""
-    parents = [int(v) for v in parents]
+    parents = [_int32(v, "a parent") for v in parents]
     T = len(parents)
     words = torch.zeros((max(T, 1), max((T + 63) // 64, 1)), dtype=torch.int64)
     host = (ctypes.c_int32 * max(T, 1))(*parents)
@@ -724,13 +739,13 @@ def tp_tree_mask(parents) -> torch.Tensor:
 
 def tp_attn_tree_workspace_bytes(T: int, past: int, n_q_heads: int, n_kv_heads: int,
                                  head_dim: int) -> int:
-    return int(load().tp_attn_tree_workspace_bytes(int(T), int(past), int(n_q_heads),
+    return int(load().tp_attn_tree_workspace_bytes(_int32(T, "T"), _int32(past, "past"), int(n_q_heads),
                                                    int(n_kv_heads), int(head_dim)))
 
 
 def tp_attn_decode_kv8_workspace_bytes(T: int, past: int, n_q_heads: int, n_kv_heads: int,
                                        head_dim: int) -> int:
-    return int(load().tp_attn_decode_kv8_workspace_bytes(int(T), int(past), int(n_q_heads),
+    return int(load().tp_attn_decode_kv8_workspace_bytes(_int32(T, "T"), _int32(past, "past"), int(n_q_heads),
                                                          int(n_kv_heads), int(head_dim)))
 
 
@@ -738,7 +753,7 @@ def tp_attn_tree_workspace_bytes_upto(T: int, max_past: int, n_q_heads: int, n_k
                                       head_dim: int) -> int:
     """Enough for tp_attn_tree and tp_attn_decode_kv8 after any number of cached
     tokens up to max_past; what the two above give may fall as `past` grows."""
-    return int(load().tp_attn_tree_workspace_bytes_upto(int(T), int(max_past), int(n_q_heads),
+    return int(load().tp_attn_tree_workspace_bytes_upto(_int32(T, "T"), _int32(max_past, "max_past"), int(n_q_heads),
                                                         int(n_kv_heads), int(head_dim)))
 
 
@@ -753,7 +768,7 @@ def _tree_workspace(name: str, T: int, blocks: int, n_q_heads: int, n_kv_heads: 
 
 def _tree_call(name, qkv, cache_ptrs, T, max_len, past, n_q_heads, n_kv_heads, head_dim, tp_degree,
                tree_mask, ctx, workspace, stream, dev) -> torch.Tensor:
-    past, nq, nkv, d = int(past), int(n_q_heads), int(n_kv_heads), int(head_dim)
+    past, nq, nkv, d = _int32(past, "past"), int(n_q_heads), int(n_kv_heads), int(head_dim)
     mask = None
     if tree_mask is not None:
         _expect_shape(tree_mask, "tree_mask", (T, (T + 63) // 64))
