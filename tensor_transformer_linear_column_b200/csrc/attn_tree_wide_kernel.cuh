@@ -68,7 +68,7 @@ struct WideShape {
   static constexpr int kTileRows = kShared ? 256 : 128; // rows of a block
   static constexpr int kQBytes = (kShared ? 2 : 1) * 32768;
   static constexpr int kValueBytes = k8 ? 2 * 32768 : 0;  // two blocks' values as fp16
-  static constexpr int kScaleBytes = k8 ? 2 * 2 * 3 * 128 * 4 : 0;  // [tile][slot][3][128]
+  static constexpr int kScaleBytes = k8 ? (2 * 2 * 3 + 2) * 128 * 4 : 0;  // [tile][slot][3][128], c
   static constexpr int kSmallBytes = kScaleBytes + 256 * 4 + 384;
   static constexpr int kFit =
       (227 * 1024 - 1024 - kSmallBytes - kQBytes - kValueBytes) / kTreeStageBytes;
@@ -372,9 +372,13 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
     const int mine = kShared ? nbc : (nbc - t + 1) / 2;  // this tile's units
     auto key_of = [&](int k) { return key0 + (kShared ? k : 2 * k + t) * 128; };
 
-    float m = kUnsetMax, l = 0.0f;  // weights are 2^(score - m - c); c is 0 but for 8 bits
-    float c = 0.0f;                 // and far scores
-    bool far = false;               // any of the warp's rows
+    // weights are 2^(score - m - c).  c is 0 but over 8 bits and for far scores, and not
+    // worth a register: held in one, some of the others spilled (188 us instead of 186
+    // for 64 tokens over 65536)
+    float m = kUnsetMax, l = 0.0f;
+    float* const c_at = sc_s + 2 * 2 * 3 * 128 + t * 128 + r;
+    if constexpr (k8) *c_at = 0.0f;
+    bool far = false;  // any of the warp's rows
     bool ok = true;
     float k_next = 0.0f, v_next = 0.0f;
     const size_t sc_row = static_cast<size_t>(g) * p.max_len + r;
@@ -447,6 +451,7 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
           float2 e[16];
           const float2 nm = make_float2(-m, -m);
           if constexpr (careful) {  // far scores, or the cache's end
+            const float c = k8 ? *c_at : 0.0f;
             products(sv, base + col, e);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -529,17 +534,18 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
               const float by = fmaxf(product - kWideProductLog2,
                                      (is_far ? 0.0f : high) - kWideWeightLog2);
               if (is_far)
-                cn = rintf(by);  // a power of two, for the partial
+                cn = rintf(fminf(by, 126.0f));  // a power of two, for the partial
               else
                 mn = by;
             }
+            const float c = k8 ? *c_at : 0.0f;
             const float rise = (mn - m) + (cn - c);
             const bool up = need && rise > 0.0f;
             // in two steps: an 8-bit row's reference may rise by more than fp32's exponents
             const float part = up ? exp2f(-0.5f * rise) : 1.0f;
             l = l * part * part;
             m = up ? mn : m;
-            c = up ? cn : c;
+            if (k8 && up) *c_at = cn;
             far = __any_sync(0xffffffffu, fabsf(m) > kWideFarScore && m != kUnsetMax);
             // O holds the products of the tile's earlier units and of this one's
             // first half: wait for that one
@@ -591,7 +597,7 @@ __global__ void __launch_bounds__(wide_threads(k8), 1)
     const bool far_row = fabsf(m) > kWideFarScore;
     const int le = static_cast<int>((__float_as_uint(l) >> 23) & 0xFFu) - 127;
     int shift = l > 0.0f && le > -127 && le < 128 ? (le < -126 ? -126 : le > 126 ? 126 : le) : 0;
-    if (far_row) shift = -static_cast<int>(c);
+    if (far_row) shift = k8 ? -static_cast<int>(*c_at) : 0;
     const float down = pow2i(-shift);
     const size_t part = (static_cast<size_t>(grp) * p.nkv + g) * p.chunks * (kShared ? 1 : 2) +
                         (kShared ? chunk : 2 * chunk + t);
