@@ -56,8 +56,9 @@
 // unrounded ones, in fp32.
 //
 // Up to 64 query rows per head the cache's bytes bound it (64 / 8 heads, 65536
-// cached tokens): 4 tokens over bf16 46 us (5.9 TB/s, 91 % of a plain copy's
-// rate), over 8 bits 34 us (4.1 TB/s).  About 7 us of a call are not the cache's: the
+// cached tokens): 4 tokens over bf16 47 us (5.7 TB/s, 89 % of a plain copy's
+// rate).  Over 8 bits a block's chain of latencies for each key block does: 34 us (4.1
+// TB/s), and 32 for 1 token with half the softmax work.  About 7 us of a call are not the cache's: the
 // launches, the first loads' latency, the last block's end (5 us after the first's
 // over a long cache: the SMs do not get the same bandwidth), the merge.
 #pragma once

@@ -24,7 +24,8 @@
 //   O_t += P_t V_b              tcgen05.mma, V read MN-major as it lies
 // A tile waits for its own two products, and the other tile's exponentials fill
 // that time.  64 tokens of 64 / 8 heads over 65536 cached tokens (512 rows per head):
-// 139 us, 990 TFLOP/s; 4,100 cycles for 256 rows of a key block, of which the softmax
+// 139 us, 990 TFLOP/s, in a burst, and 164 (840) after some hundred calls in a row,
+// when the power cap holds the clock down; 4,100 cycles for 256 rows of a key block, of which the softmax
 // of a tile takes 2,300 and its products 1,600.  On the way: keys as M and weights
 // through shared memory 312 us; rows as M 180; bf16 weights over the scores in
 // tensor memory instead of in shared memory, the ring twice as deep 177; the issuing
@@ -34,7 +35,7 @@
 // all rows, and a row's weights times the value scales are fp16 against those
 // (within 2^-11, plus 2^-26 of the largest product; splitting them into three E5M2
 // terms, as for few rows, costs three of eight instructions an element: 266 us instead
-// of 184 for 64 tokens over 65536 rows).  A row's m bounds the products p * scale
+// of 186 for 64 tokens over 65536 rows).  A row's m bounds the products p * scale
 // themselves, so a key of a large value scale and a small weight costs the others
 // nothing.
 #pragma once
