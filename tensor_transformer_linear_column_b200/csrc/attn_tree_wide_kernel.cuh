@@ -25,11 +25,11 @@
 // A tile waits for its own two products, and the other tile's exponentials fill
 // that time.  64 tokens of 64 / 8 heads over 65536 cached tokens (512 rows per head):
 // 139 us, 990 TFLOP/s, in a burst, and 164 (840) after some hundred calls in a row,
-// when the power cap holds the clock down; 4,100 cycles for 256 rows of a key block, of which the softmax
-// of a tile takes 2,300 and its products 1,600.  On the way: keys as M and weights
-// through shared memory 312 us; rows as M 180; bf16 weights over the scores in
-// tensor memory instead of in shared memory, the ring twice as deep 177; the issuing
-// warp converged 158; weights handed over by halves 139.
+// when the power cap holds the clock down; 4,100 cycles for 256 rows of a key block,
+// of which the softmax of a tile takes 2,300 and its products 1,600.  On the way: keys
+// as M and weights through shared memory 312 us; rows as M 180; bf16 weights over the
+// scores in tensor memory instead of in shared memory, the ring twice as deep 177; the
+// issuing warp converged 158; weights handed over by halves 139.
 // 8-bit caches: scores as in attn_tree_kernel (queries in two E4M3 parts against
 // the codes); here two more warps turn each block's value codes into fp16 once for
 // all rows, and a row's weights times the value scales are fp16 against those
